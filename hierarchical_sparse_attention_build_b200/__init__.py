@@ -1,6 +1,7 @@
 """Python binding of librecsa: RecSA tree build and level-wise sparse attend on B200.
 
-Thin ctypes marshalling over the C ABI declared in ``include/recsa.h``; every step of
+Thin ctypes marshalling over the C ABI declared in ``include/recsa.h`` and
+``include/recsa_dense.h``; every step of
 the computation runs in the library's CUDA kernels.  PyTorch supplies device memory
 and the current CUDA stream.  Importing this module fails loudly when the compiled
 library is missing: there is no CPU fallback.
@@ -104,6 +105,13 @@ def _load() -> ctypes.CDLL:
         "recsa_prefill_chunk": [P, T, vp, vp, vp, i32, vp, i32, vp, sz, D, vp],
         "recsa_check_device_errors": [vp, vp],
         "recsa_decode_no_alloc": [P, T, vp, i32, vp, i32, vp],
+        "recsa_dense_workspace_size": [P, i32, i64, ctypes.POINTER(sz)],
+        "recsa_dense_workspace_init": [P, i32, i64, vp, sz, vp],
+        "recsa_dense_attend": [P, T, vp, vp, i32, vp, i32, vp, sz, vp],
+        "recsa_dense_prefill_chunk": [P, T, vp, vp, vp, vp, i32, vp, i32, vp, sz, vp],
+        "recsa_dense_decode_step": [P, T, vp, vp, vp, vp, vp, i32, vp, sz, vp],
+        "recsa_accumulate_weights": [P, T, vp, vp, i32, vp, i32, vp, sz, vp],
+        "recsa_evict": [P, T, vp, i32, i32, i32, vp, T, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -304,6 +312,173 @@ def decode_no_alloc(p: Params, tree: RecsaTree, q: torch.Tensor, out: torch.Tens
 
 def check_device_errors(ws: Workspace, stream=None) -> None:
     _check(_lib.recsa_check_device_errors(_ptr(ws.buf), _stream(stream)))
+
+
+# --------------------------------------------------------------------------- dense operators
+
+
+class View(ctypes.Structure):
+    """recsa_view: which tokens a dense query sees.
+
+    window = 0 sees every token before the query; otherwise the last `window` tokens and the
+    first `sinks`.  causal: the queries belong to the cache's last tokens (else all sit at its
+    end); own_token: a causal query also sees its own token.  token_positions: sinks outside
+    the window are scored at their token positions instead of their rank among the visible."""
+
+    _fields_ = [
+        ("sinks", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sink_positions", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("own_token", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+    def __init__(self, sinks: int = 0, window: int = 0, causal: bool = False, own_token: bool = False,
+                 token_positions: bool = False):
+        super().__init__(sinks, window, int(token_positions), int(causal), int(own_token), 0)
+
+
+class TokenCache(RecsaTree):
+    """Token caches without a tree, for layers that only run the dense operators (those also
+    take a RecsaTree, whose tree they keep up to date)."""
+
+    def __init__(self, p: Params, k_tok: torch.Tensor, v_tok: torch.Tensor, length: int,
+                 seq_len: torch.Tensor | None = None, page_table: torch.Tensor | None = None):
+        """Arguments as RecsaTree's."""
+        none = torch.empty(0, dtype=torch.float32, device=k_tok.device)
+        super().__init__(p, k_tok, v_tok, none, length, k_node=none, v_node=none, seq_len=seq_len,
+                         page_table=page_table)
+        self.k_node = self.v_node = self.pooler = None
+        self.c.k_node = self.c.v_node = self.c.pooler = None
+
+
+def dense_workspace_size(p: Params, batch: int, capacity: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.recsa_dense_workspace_size(ctypes.byref(p), batch, capacity, ctypes.byref(n)))
+    return n.value
+
+
+class DenseWorkspace:
+    """Workspace of the dense operators on caches of `batch` sequences of up to `capacity`
+    tokens.  Every call writes it: one per stream (or captured graph) that may overlap."""
+
+    def __init__(self, p: Params, batch: int, capacity: int, device, stream=None, buffer: torch.Tensor | None = None):
+        self.nbytes = dense_workspace_size(p, batch, capacity)
+        self.buf = buffer if buffer is not None else torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        if not self.buf.is_cuda:
+            raise RecsaError(1, "the workspace is not on a CUDA device")
+        _on_current_device(self.buf)
+        _check(_lib.recsa_dense_workspace_init(ctypes.byref(p), batch, capacity, _ptr(self.buf),
+                                               self.buf.numel() * self.buf.element_size(), _stream(stream)))
+
+
+def _on_current_device(*tensors: torch.Tensor) -> None:
+    """The library launches on the current device: every tensor has to be on it."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != dev:
+            raise RecsaError(1, f"a tensor on {t.device}, the current device is cuda:{dev}")
+
+
+def _dense_rows(p: Params, tree: RecsaTree, t: torch.Tensor, heads: int, name: str, dtypes=(torch.bfloat16,)) -> None:
+    """t is [batch][n][heads][128], contiguous, of one of the types."""
+    if t.dtype not in dtypes:
+        raise RecsaError(1, f"{name} is {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != tree.batch or t.shape[2] != heads or t.shape[3] != HEAD_DIM:
+        raise RecsaError(1, f"{name} has shape {tuple(t.shape)}, not [{tree.batch}][n][{heads}][{HEAD_DIM}]")
+    if not t.is_contiguous():
+        raise RecsaError(1, f"{name} is not contiguous")
+
+
+_OUT_TYPES = (torch.float32, torch.bfloat16)
+
+
+def _dense_q(p: Params, tree: RecsaTree, q: torch.Tensor, out: torch.Tensor, ws: DenseWorkspace) -> None:
+    _dense_rows(p, tree, q, p.num_q_heads, "q")
+    _dense_rows(p, tree, out, p.num_q_heads, "out", _OUT_TYPES)
+    if out.shape != q.shape:
+        raise RecsaError(1, f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
+    _on_current_device(tree.k_tok, q, out, ws.buf)
+
+
+def _dense_new(p: Params, tree: RecsaTree, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor) -> None:
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _dense_rows(p, tree, t, p.num_kv_heads, name)
+        if t.shape[1] != q.shape[1]:
+            raise RecsaError(1, f"{name} holds {t.shape[1]} tokens, q {q.shape[1]}")
+        _on_current_device(t)
+
+
+def _view(view: View | None):
+    return None if view is None else ctypes.byref(view)
+
+
+def dense_attend(p: Params, tree: RecsaTree, q: torch.Tensor, out: torch.Tensor, ws: DenseWorkspace,
+                 view: View | None = None, stream=None) -> None:
+    """recsa_dense_attend: q [B][n][Hq][128] bf16 over the cache's tokens -> out of the same
+    shape (fp32 or bf16)."""
+    _dense_q(p, tree, q, out, ws)
+    _check(_lib.recsa_dense_attend(ctypes.byref(p), ctypes.byref(tree.c), _view(view), _ptr(q), q.shape[1], _ptr(out),
+                                   int(out.dtype == torch.float32), _ptr(ws.buf), ws.nbytes, _stream(stream)))
+
+
+def dense_prefill_chunk(p: Params, tree: RecsaTree, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor,
+                        out: torch.Tensor, ws: DenseWorkspace, view: View | None = None, stream=None) -> None:
+    """recsa_dense_prefill_chunk: append [B][C][Hkv][128] K/V, attend the C queries causally."""
+    _dense_q(p, tree, q, out, ws)
+    _dense_new(p, tree, k_new, v_new, q)
+    _check(_lib.recsa_dense_prefill_chunk(ctypes.byref(p), ctypes.byref(tree.c), _view(view), _ptr(k_new), _ptr(v_new),
+                                          _ptr(q), q.shape[1], _ptr(out), int(out.dtype == torch.float32),
+                                          _ptr(ws.buf), ws.nbytes, _stream(stream)))
+
+
+def dense_decode_step(p: Params, tree: RecsaTree, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor,
+                      out: torch.Tensor, ws: DenseWorkspace, view: View | None = None, stream=None) -> None:
+    """recsa_dense_decode_step: append one token per sequence at its device length, advance the
+    lengths, attend the token's query; graph-capturable (needs tree.seq_len)."""
+    _dense_q(p, tree, q, out, ws)
+    _dense_new(p, tree, k_new, v_new, q)
+    if q.shape[1] != 1:
+        raise RecsaError(1, f"a decode step takes one token per sequence, not {q.shape[1]}")
+    _check(_lib.recsa_dense_decode_step(ctypes.byref(p), ctypes.byref(tree.c), _view(view), _ptr(k_new), _ptr(v_new),
+                                        _ptr(q), _ptr(out), int(out.dtype == torch.float32), _ptr(ws.buf), ws.nbytes,
+                                        _stream(stream)))
+
+
+def _weights_of(tree: RecsaTree, w: torch.Tensor, name: str) -> None:
+    if w.dtype != torch.float32 or not w.is_contiguous() or tuple(w.shape) != (
+            tree.batch, tree.p.num_kv_heads, tree.capacity):
+        raise RecsaError(1, f"{name} is {w.dtype} {tuple(w.shape)}, not contiguous float32 "
+                            f"[{tree.batch}][{tree.p.num_kv_heads}][{tree.capacity}]")
+    _on_current_device(w)
+
+
+def accumulate_weights(p: Params, tree: RecsaTree, q: torch.Tensor, weights: torch.Tensor, ws: DenseWorkspace,
+                       view: View | None = None, accumulate: bool = True, stream=None) -> None:
+    """recsa_accumulate_weights: the softmax weight each slot receives from q [B][n][Hq][128],
+    summed over queries and group heads, into weights [B][Hkv][capacity] (fp32)."""
+    _dense_rows(p, tree, q, p.num_q_heads, "q")
+    _weights_of(tree, weights, "weights")
+    _on_current_device(tree.k_tok, q, ws.buf)
+    _check(_lib.recsa_accumulate_weights(ctypes.byref(p), ctypes.byref(tree.c), _view(view), _ptr(q), q.shape[1],
+                                         _ptr(weights), int(accumulate), _ptr(ws.buf), ws.nbytes, _stream(stream)))
+
+
+def evict(p: Params, tree: RecsaTree, weights: torch.Tensor, keep: int, kept: torch.Tensor,
+          into: RecsaTree | None = None, into_weights: torch.Tensor | None = None, sinks: int = 0, recent: int = 0,
+          stream=None) -> None:
+    """recsa_evict: cut every (sequence, KV head) to its `keep` heaviest slots, in place or into
+    another cache; kept [B][Hkv][keep] int32 receives the kept slots."""
+    _weights_of(tree, weights, "weights")
+    if kept.dtype != torch.int32 or not kept.is_contiguous() or tuple(kept.shape) != (tree.batch, p.num_kv_heads, keep):
+        raise RecsaError(1, f"kept is {kept.dtype} {tuple(kept.shape)}, not contiguous int32 "
+                            f"[{tree.batch}][{p.num_kv_heads}][{keep}]")
+    if into_weights is not None:
+        _weights_of(tree if into is None else into, into_weights, "into_weights")
+    _on_current_device(tree.k_tok, kept, *(() if into is None else (into.k_tok,)))
+    _check(_lib.recsa_evict(ctypes.byref(p), ctypes.byref(tree.c), _ptr(weights), keep, sinks, recent, _ptr(kept),
+                            None if into is None else ctypes.byref(into.c), _ptr(into_weights), _stream(stream)))
 
 
 def status_string(code: int) -> str:

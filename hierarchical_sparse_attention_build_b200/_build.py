@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librecsa.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
-SOURCES = ["recsa_abi.cpp", "recsa_build.cu", "recsa_attend.cu", "recsa_no_alloc.cu"]
+SOURCES = ["recsa_abi.cpp", "recsa_dense_abi.cpp", "recsa_build.cu", "recsa_attend.cu", "recsa_no_alloc.cu",
+           "recsa_dense.cu", "recsa_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
 
@@ -29,7 +30,7 @@ def nvcc() -> str:
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    files.append(os.path.join(INCLUDE, "recsa.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -39,9 +39,7 @@ int levels_for(int64_t length, int b) {
 
 }  // namespace recsa
 
-using namespace recsa;
-
-namespace {
+namespace recsa {
 
 recsa_status fail(recsa_status s, const char *fmt, ...) {
   char buf[480];
@@ -127,7 +125,7 @@ size_t workspace_bytes(const recsa_params *p, int64_t capacity) {
   return kWsHeader + (size_t)table_rows_for(p, capacity) * kHalf * sizeof(float) * 2;
 }
 
-recsa_status check_tree(const recsa_params *p, const recsa_tree *t, TreeGeom *g) {
+recsa_status check_tree(const recsa_params *p, const recsa_tree *t, TreeGeom *g, bool cache_only) {
   if (!t) return fail(RECSA_ERR_INVALID_ARGUMENT, "tree is NULL");
   recsa_status s = make_geom(p, t->batch, t->capacity, g);
   if (s != RECSA_OK) return s;
@@ -136,7 +134,7 @@ recsa_status check_tree(const recsa_params *p, const recsa_tree *t, TreeGeom *g)
                 (long long)t->capacity);
   const void *ptrs[5] = {t->k_tok, t->v_tok, t->k_node, t->v_node, t->pooler};
   const char *names[5] = {"k_tok", "v_tok", "k_node", "v_node", "pooler"};
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < (cache_only ? 2 : 5); ++i) {
     if (!ptrs[i]) return fail(RECSA_ERR_INVALID_ARGUMENT, "tree->%s is NULL", names[i]);
     if (!aligned16(ptrs[i])) return fail(RECSA_ERR_INVALID_ARGUMENT, "tree->%s is not 16-byte aligned", names[i]);
   }
@@ -257,7 +255,9 @@ recsa_status decode_launch(const recsa_params *params, const recsa_tree *tree, c
   return RECSA_OK;
 }
 
-}  // namespace
+}  // namespace recsa
+
+using namespace recsa;
 
 extern "C" {
 

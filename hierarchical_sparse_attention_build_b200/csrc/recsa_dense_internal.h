@@ -1,0 +1,55 @@
+// Host declarations of the dense cache operators: the workspace layout, the arguments of a
+// launch and the launchers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "recsa_dense.h"
+#include "recsa_internal.h"
+
+namespace recsa {
+
+constexpr uint32_t kDenseMagic = 0x52534432u;  // "RSD2"
+constexpr int kSpan = 64;                      // positions of the rotation table
+constexpr int kMaxShared = 4096;               // work items whose key range may be shared by blocks
+constexpr size_t kDenseFreq = kWsHeader;                                   // uint64[64] turns
+constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float2[64][64] (cos, sin)
+constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
+constexpr size_t kDensePart = kDenseCount + kMaxShared * sizeof(int32_t);  // partial results
+constexpr size_t kDensePartBytes = (size_t)40 << 20;
+constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
+constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call
+constexpr size_t kDenseBytes = kDenseLse + kMaxDenseLse * sizeof(float);
+constexpr int kPartRow = kD + 4;  // floats of a row's partial result: maximum, sum, 2 unused, 128 sums
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The cache and the queries of one launch.
+struct DenseArgs {
+  const uint16_t *k, *v, *q;
+  void *out;
+  const int64_t *seq_len;
+  const int32_t *pages;
+  int64_t capacity;
+  int32_t pages_per_seq, page_shift, num_pages;
+  int32_t batch, hkv, group_shift, nq;
+  int32_t length;
+  int32_t sinks, window, rank_sinks, causal, own;
+  int32_t out_fp32;
+  int32_t tiles, nsplit;
+  float qscale;       // softmax scale * log2(e)
+  float rope_base;
+  WsHeader *hdr;
+};
+
+int dense_sm_count();  // of the current device
+int launch_dense_init(void *ws, double base, void *stream);
+int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, void *stream);
+int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream);
+int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
+                         int count, int64_t limit, void *stream);
+// Partial results a launch may leave in the workspace.
+constexpr int64_t kRowsParts = (int64_t)(kDensePartBytes / (16 * kPartRow * sizeof(float)));
+
+}  // namespace recsa

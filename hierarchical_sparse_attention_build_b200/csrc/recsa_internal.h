@@ -48,6 +48,17 @@ struct Status {
 void set_error(const char *fmt, ...);
 int64_t ceil_div(int64_t a, int64_t b);
 int levels_for(int64_t length, int b);  // T(length)
+recsa_status fail(recsa_status s, const char *fmt, ...);  // records the message, returns s
+recsa_status cuda_fail(int rc, const char *what);
+bool aligned16(const void *p);
+recsa_status check_params(const recsa_params *p);
+recsa_status make_geom(const recsa_params *p, int32_t batch, int64_t capacity, TreeGeom *g);
+// cache_only: the token caches, lengths and page table alone (the node arena is not looked at)
+recsa_status check_tree(const recsa_params *p, const recsa_tree *t, TreeGeom *g, bool cache_only = false);
+recsa_status build_range(const TreeGeom &g, const recsa_tree &t, int64_t length, int64_t old_length, bool extension,
+                         void *stream);
+recsa_status extend_tree(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t L,
+                         int chunk, void *stream);
 
 // Launchers (return cudaError_t as int; 0 = success)
 int launch_rope_table(void *ws, int rows, double base, void *stream);
