@@ -167,7 +167,7 @@ __device__ __forceinline__ Range tile_range(const DenseArgs &a, int p_min, int p
 // K and V bounds it: at G = 4 a key costs 512 bytes and about 45 issue slots of its SM's ~88.
 // PV: values are weighted and summed; without it the rows' log2-sum-exp goes to `lse`.
 template <bool SPLIT, bool PV>
-__global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, float *lse) {
+__global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, float *lse, const uint32_t *redo, int chunk_tiles) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   RowsSmem &sm = *reinterpret_cast<RowsSmem *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -180,6 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, fl
   if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) {
     if (tid == 0) atomicOr(&a.hdr->err, kErrWs);
     return;
+  }
+  if (redo) {  // only what the chunk kernel marked
+    const int chunk_item = bh * chunk_tiles + chunk_tiles - 1 - q0 / (256 >> gs);
+    if (!redo[chunk_item % kMaxShared]) return;
   }
   const int len = dense_length(a, b, tid == 0 && tile == 0 && split == 0 && h == 0);
   const int p_min = dense_position(a, len, q0), p_max = dense_position(a, len, q0 + nq - 1);
@@ -644,7 +648,10 @@ __global__ void dense_init_kernel(unsigned char *ws, double base) {
     const double turns = theta / (2.0 * 3.14159265358979323846);
     reinterpret_cast<uint64_t *>(ws + kDenseFreq)[i] = (uint64_t)((turns - floor(turns)) * 18446744073709551616.0);
   }
-  if (idx < kMaxShared) reinterpret_cast<int32_t *>(ws + kDenseCount)[idx] = 0;
+  if (idx < kMaxShared) {
+    reinterpret_cast<int32_t *>(ws + kDenseCount)[idx] = 0;
+    reinterpret_cast<uint32_t *>(ws + kDenseRedo)[idx] = 0u;
+  }
   if (idx == 0) {
     hdr->err = 0u;
     hdr->table_rows = kSpan;
@@ -660,10 +667,11 @@ int opt_in(K kernel, size_t bytes) {
 }
 
 template <bool SPLIT, bool PV>
-int run_rows(const DenseArgs &a, unsigned grid, float *lse, void *stream) {
+int run_rows(const DenseArgs &a, unsigned grid, float *lse, void *stream, const uint32_t *redo = nullptr,
+             int chunk_tiles = 0) {
   int rc = opt_in(dense_rows_kernel<SPLIT, PV>, sizeof(RowsSmem));
   if (rc) return rc;
-  dense_rows_kernel<SPLIT, PV><<<grid, kThreads, sizeof(RowsSmem), (cudaStream_t)stream>>>(a, lse);
+  dense_rows_kernel<SPLIT, PV><<<grid, kThreads, sizeof(RowsSmem), (cudaStream_t)stream>>>(a, lse, redo, chunk_tiles);
   return (int)cudaGetLastError();
 }
 
@@ -711,6 +719,16 @@ int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, voi
   const unsigned grid = (unsigned)(items * a.nsplit);
   if (lse) return run_rows<true, false>(a, grid, lse, stream);
   return split ? run_rows<true, true>(a, grid, nullptr, stream) : run_rows<false, true>(a, grid, nullptr, stream);
+}
+
+int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream) {
+  const int per = kRows >> a.group_shift;
+  a.tiles = (a.nq + per - 1) / per;
+  a.nsplit = 1;
+  uint32_t *redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(a.hdr) + kDenseRedo);
+  int rc = run_rows<true, true>(a, (unsigned)((int64_t)a.batch * a.hkv * a.tiles), nullptr, stream, redo, chunk_tiles);
+  if (rc) return rc;
+  return (int)cudaMemsetAsync(redo, 0, kMaxShared * sizeof(uint32_t), (cudaStream_t)stream);
 }
 
 int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream) {

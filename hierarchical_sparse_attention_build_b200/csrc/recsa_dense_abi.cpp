@@ -83,6 +83,9 @@ DenseArgs dense_args(const recsa_params *p, const recsa_tree *t, const recsa_vie
   return a;
 }
 
+// Query rows of a KV group from which the chunk kernel's tiles of 256 rows take over.
+constexpr int64_t kChunkRows = 64;
+
 // The work items of the launch fit its grid.
 recsa_status check_rows(const DenseArgs &a) {
   const int64_t rows = ((int64_t)a.nq << a.group_shift) * a.hkv * a.batch;
@@ -95,13 +98,15 @@ recsa_status check_rows(const DenseArgs &a) {
 int64_t max_keys(const DenseArgs &a) {
   const int64_t n = a.length;
   if (!a.window) return n;
-  return std::min<int64_t>(n, (int64_t)a.sinks + a.window + 16);
+  return std::min<int64_t>(n, (int64_t)a.sinks + a.window + (a.causal ? std::min(a.nq, 256 >> a.group_shift) : 0));
 }
 
 recsa_status attend(DenseArgs a, void *out, int32_t out_is_fp32, void *stream) {
   a.out = out;
   a.out_fp32 = out_is_fp32 ? 1 : 0;
-  const int rc = launch_dense_rows(a, a.out_fp32 != 0, max_keys(a), nullptr, stream);
+  const int64_t rows = (int64_t)a.nq << a.group_shift;  // of a KV group
+  const int rc = !a.out_fp32 && rows >= kChunkRows ? launch_dense_chunk(a, max_keys(a), stream)
+                                                   : launch_dense_rows(a, a.out_fp32 != 0, max_keys(a), nullptr, stream);
   return rc != 0 ? cuda_fail(rc, "dense attend") : RECSA_OK;
 }
 

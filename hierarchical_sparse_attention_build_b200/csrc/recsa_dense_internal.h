@@ -16,7 +16,8 @@ constexpr int kMaxShared = 4096;               // work items whose key range may
 constexpr size_t kDenseFreq = kWsHeader;                                   // uint64[64] turns
 constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float2[64][64] (cos, sin)
 constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
-constexpr size_t kDensePart = kDenseCount + kMaxShared * sizeof(int32_t);  // partial results
+constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t);  // marks of items to compute again
+constexpr size_t kDensePart = kDenseRedo + kMaxShared * sizeof(uint32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
 constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call
@@ -46,6 +47,9 @@ struct DenseArgs {
 int dense_sm_count();  // of the current device
 int launch_dense_init(void *ws, double base, void *stream);
 int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, void *stream);
+// The chunk kernel (bf16 output), then the rows kernel for the items it marked.
+int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, void *stream);
+int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
 int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
                          int count, int64_t limit, void *stream);
