@@ -101,11 +101,11 @@ int64_t max_keys(const DenseArgs &a) {
   return std::min<int64_t>(n, (int64_t)a.sinks + a.window + (a.causal ? std::min(a.nq, 256 >> a.group_shift) : 0));
 }
 
-recsa_status attend(DenseArgs a, void *out, int32_t out_is_fp32, void *stream) {
+recsa_status attend(DenseArgs a, void *out, int32_t out_is_fp32, size_t ws_bytes, void *stream) {
   a.out = out;
   a.out_fp32 = out_is_fp32 ? 1 : 0;
   const int64_t rows = (int64_t)a.nq << a.group_shift;  // of a KV group
-  const int rc = !a.out_fp32 && rows >= kChunkRows ? launch_dense_chunk(a, max_keys(a), stream)
+  const int rc = !a.out_fp32 && rows >= kChunkRows ? launch_dense_chunk(a, max_keys(a), (int64_t)(ws_bytes - kDenseImages), stream)
                                                    : launch_dense_rows(a, a.out_fp32 != 0, max_keys(a), nullptr, stream);
   return rc != 0 ? cuda_fail(rc, "dense attend") : RECSA_OK;
 }
@@ -123,7 +123,10 @@ RECSA_API recsa_status recsa_dense_workspace_size(const recsa_params *params, in
   if (capacity > ((int64_t)1 << 30))
     return fail(RECSA_ERR_UNSUPPORTED, "capacity %lld > 2^30 tokens", (long long)capacity);
   if (!bytes_out) return fail(RECSA_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
-  *bytes_out = kDenseBytes;
+  // rotated images: the keys of every head, and as many rows of every query head
+  const int64_t rows = std::min<int64_t>((capacity + 127) / 128 * 128 * batch, 1 << 20);
+  const int64_t images = rows * (params->num_kv_heads + 2 * (int64_t)params->num_q_heads) * kRowBytes + (1 << 20);
+  *bytes_out = kDenseImages + (size_t)std::min<int64_t>(images, kMaxDenseImages);
   return RECSA_OK;
 }
 
@@ -155,7 +158,7 @@ RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recs
                                  view && view->own_token, ws);
   s = check_rows(a);
   if (s != RECSA_OK) return s;
-  return attend(a, out, out_is_fp32, stream);
+  return attend(a, out, out_is_fp32, ws_bytes, stream);
 }
 
 RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, recsa_tree *tree, const recsa_view *view,
@@ -193,7 +196,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
     rc = launch_advance_lengths(tree->seq_len, tree->batch, chunk, L2, stream);
     if (rc != 0) return cuda_fail(rc, "advance of the sequence lengths");
   }
-  s = attend(a, out, out_is_fp32, stream);
+  s = attend(a, out, out_is_fp32, ws_bytes, stream);
   if (s == RECSA_OK) tree->length = L2;
   return s;
 }
@@ -224,7 +227,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
   if (rc != 0) return cuda_fail(rc, "append");
   rc = launch_advance_lengths(tree->seq_len, tree->batch, 1, cap, stream);
   if (rc != 0) return cuda_fail(rc, "advance of the sequence lengths");
-  return attend(a, out, out_is_fp32, stream);
+  return attend(a, out, out_is_fp32, ws_bytes, stream);
 }
 
 RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, const recsa_tree *tree,

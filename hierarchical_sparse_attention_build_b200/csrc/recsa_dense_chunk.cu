@@ -32,11 +32,11 @@ constexpr int kTile = 128;                  // rows of a row tile, keys of a key
 constexpr int kItemRows = 2 * kTile;
 constexpr int kSoftWarps = 8;
 constexpr int kLoadThreads = 128;
-constexpr int kChunkThreads = 13 * 32;
 constexpr int kTileBytes = kTile * kRowBytes;  // 32 KB: [64-element half][row][128 bytes], 16-byte pieces XOR row % 8
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kRing = 2;                    // key and value tiles in shared memory
 constexpr int kMaxChunkBlocks = (int)(kDensePartBytes / (2 * kItemRows * kPartRow * sizeof(float)));
+constexpr int kImageTiles = 2;              // items a head from which images are made
 constexpr float kRescale = 8.f;             // a row's maximum may lag by 2^8 before its output is rescaled
 
 struct ChunkSmem {
@@ -58,10 +58,19 @@ constexpr size_t kChunkSmem = sizeof(ChunkSmem) + 1024;  // the tiles begin on 1
 
 struct ChunkArgs {
   DenseArgs d;
+  int bh0, heads;  // the launch's (sequence, KV head) pairs
   int items;     // work items
   int shared;    // 1: the key tiles of all items are dealt out evenly to the blocks
   uint32_t *redo;
+  // rotated rows as the tiles' shared-memory images (IMG): keys [heads][key_tiles], their loaded
+  // tokens, queries [items][1 or 2: for the window's tokens, for the sinks][2 row tiles]
+  unsigned char *key_images, *query_images;
+  uint4 *live;
+  int key_tiles, query_sets;
 };
+__device__ __forceinline__ uint32_t &redo_mark(const ChunkArgs &a, int item) {
+  return a.redo[(a.bh0 * a.d.tiles + item) % kMaxShared];
+}
 
 __host__ __device__ constexpr uint32_t chunk_idesc(bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(kTile >> 3) << 17) |
@@ -115,7 +124,7 @@ struct Item {
 __device__ __forceinline__ Item chunk_item(const ChunkArgs &a, int item) {
   const DenseArgs &d = a.d;
   Item it;
-  const int bh = item / d.tiles, tile = d.tiles - 1 - item % d.tiles;  // the longest ranges first
+  const int bh = a.bh0 + item / d.tiles, tile = d.tiles - 1 - item % d.tiles;  // the longest ranges first
   it.b = bh / d.hkv;
   it.h = bh % d.hkv;
   it.q0 = tile * (kItemRows >> d.group_shift);
@@ -130,6 +139,19 @@ __device__ __forceinline__ Item chunk_item(const ChunkArgs &a, int item) {
   it.first = it.lo2 / kTile;
   it.tiles = max(1, it.n1 + (it.hi2 > it.lo2 ? (it.hi2 + kTile - 1) / kTile - it.first : 0));
   return it;
+}
+
+// The key tiles that some query of the chunk sees: those of the sinks, then the window's.
+struct HeadRange {
+  int n1, first, count;
+};
+__device__ __forceinline__ HeadRange head_range(const DenseArgs &d, int len) {
+  const int p_min = dense_position(d, len, 0), p_max = dense_position(d, len, d.nq - 1);
+  HeadRange r;
+  r.n1 = d.window ? (max(0, min(d.sinks, p_max)) + kTile - 1) / kTile : 0;
+  r.first = max(0, window_first(d, p_min)) / kTile;
+  r.count = r.n1 + max(0, (max(p_max, 0) + kTile - 1) / kTile - r.first);
+  return r;
 }
 
 // The segments (item, key tiles [j0, j1)) of this block, the same for every role.
@@ -192,20 +214,20 @@ __device__ __forceinline__ bool wait_or_stop(ChunkSmem &sm, const ChunkArgs &a, 
 
 // Rotation state of eight frequencies: cos and sin of a position, advanced by a fixed step.
 struct Turn {
-  float c[8], s[8];
+  F2 c[4], s[4];
   __device__ __forceinline__ void set(const uint64_t *f, int pos) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 r = rotation(pos, __ldg(f + i));
-      c[i] = r.x;
-      s[i] = r.y;
+    for (int i = 0; i < 4; ++i) {
+      const float2 r0 = rotation(pos, __ldg(f + 2 * i)), r1 = rotation(pos, __ldg(f + 2 * i + 1));
+      c[i] = f2(r0.x, r1.x);
+      s[i] = f2(r0.y, r1.y);
     }
   }
   __device__ __forceinline__ void advance(const Turn &d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = c[i] * d.c[i] - s[i] * d.s[i];
-      s[i] = s[i] * d.c[i] + c[i] * d.s[i];
+    for (int i = 0; i < 4; ++i) {
+      const F2 u = f2_fma(f2_neg(s[i]), d.s[i], f2_mul(c[i], d.c[i]));
+      s[i] = f2_fma(c[i], d.s[i], f2_mul(s[i], d.c[i]));
       c[i] = u;
     }
   }
@@ -213,16 +235,21 @@ struct Turn {
 
 // Dimensions 8 ch .. 8 ch + 7 and 64 more of one bf16 row, turned and rounded to fp16; `most`
 // keeps the largest magnitudes.
+template <bool SCALE>
 __device__ __forceinline__ void turn_row(const uint4 &lo, const uint4 &hi, const Turn &t, float scale, uint4 &out_lo,
                                          uint4 &out_hi, __half2 &most) {
   const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
   uint32_t u[4], v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float x0 = bf16_lo(x[i]) * scale, x1 = bf16_hi(x[i]) * scale;
-    const float y0 = bf16_lo(y[i]) * scale, y1 = bf16_hi(y[i]) * scale;
-    const __half2 a = __floats2half2_rn(x0 * t.c[2 * i] - y0 * t.s[2 * i], x1 * t.c[2 * i + 1] - y1 * t.s[2 * i + 1]);
-    const __half2 b = __floats2half2_rn(y0 * t.c[2 * i] + x0 * t.s[2 * i], y1 * t.c[2 * i + 1] + x1 * t.s[2 * i + 1]);
+    F2 p = f2_bf16(x[i]), q = f2_bf16(y[i]);
+    if (SCALE) {
+      p = f2_mul(p, f2(scale, scale));
+      q = f2_mul(q, f2(scale, scale));
+    }
+    const float2 a2 = f2_get(f2_fma(q, f2_neg(t.s[i]), f2_mul(p, t.c[i])));
+    const float2 b2 = f2_get(f2_fma(p, t.s[i], f2_mul(q, t.c[i])));
+    const __half2 a = __floats2half2_rn(a2.x, a2.y), b = __floats2half2_rn(b2.x, b2.y);
     most = __hmax2(most, __hmax2(__habs2(a), __habs2(b)));
     u[i] = *reinterpret_cast<const uint32_t *>(&a);
     v[i] = *reinterpret_cast<const uint32_t *>(&b);
@@ -237,7 +264,7 @@ __device__ __forceinline__ void put_row(unsigned char *tile, int row, int ch, co
 }
 
 // The item's query rows, turned to their positions (sinks: their positions for the sinks).
-__device__ __forceinline__ void load_queries(const ChunkArgs &a, ChunkSmem &sm, const Item &it, bool sink, int lt,
+__device__ __forceinline__ void load_queries(const ChunkArgs &a, unsigned char *q, const Item &it, bool sink, int lt,
                                              __half2 &most) {
   const DenseArgs &d = a.d;
   const int ch = lt & 7, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
@@ -259,13 +286,95 @@ __device__ __forceinline__ void load_queries(const ChunkArgs &a, ChunkSmem &sm, 
       hi = __ldg(src + ch + 8);
     }
     uint4 ol, oh;
-    turn_row(lo, hi, t, d.qscale, ol, oh, most);
-    put_row(sm.q[row >> 7], row & 127, ch, ol, oh);
+    turn_row<true>(lo, hi, t, d.qscale, ol, oh, most);
+    put_row(q + (row >> 7) * kTileBytes, row & 127, ch, ol, oh);
     if (even) t.advance(step);
   }
 }
 
-__global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs a) {
+__device__ __forceinline__ bool beyond_half(__half2 most) {
+  return __hgt(__hmax(__low2half(most), __high2half(most)), __float2half(65504.f));
+}
+
+// Rotated keys and queries of a launch as the chunk kernel's shared-memory images, so that it
+// fetches a tile with one bulk copy.  A block turns one key tile or one item's query rows.
+__global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a) {
+  const DenseArgs &d = a.d;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the chunk kernel reports it
+  const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3;
+  __half2 most = __floats2half2_rn(0.f, 0.f);
+  const int keys = a.heads * a.key_tiles;
+  if ((int)blockIdx.x >= keys) {
+    const int e = blockIdx.x - keys, item = e / a.query_sets;
+    load_queries(a, a.query_images + (int64_t)e * (2 * kTileBytes), chunk_item(a, item), e % a.query_sets == 1, lt, most);
+    if (beyond_half(most)) redo_mark(a, item) = 1u;
+    return;
+  }
+  const int hl = blockIdx.x / a.key_tiles, kt = blockIdx.x % a.key_tiles;
+  const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
+  const int len = dense_length(d, b, false);
+  const HeadRange hr = head_range(d, len);
+  if (kt >= hr.count) return;
+  const int T = (kt < hr.n1 ? kt : hr.first + kt - hr.n1) * kTile;
+  unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kTileBytes;
+  Turn t, step;
+  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
+  t.set(f, T + r0);
+  step.set(f, 16);
+  uint32_t word[4] = {0u, 0u, 0u, 0u};
+  uint4 xl[8], xh[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int tok = T + r0 + 16 * i;
+    xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
+    if (tok < len) {
+      const int64_t r = cache_row(d, b, h, tok);
+      if (r >= 0) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
+        xl[i] = __ldg(src + ch);
+        xh[i] = __ldg(src + ch + 8);
+        word[i >> 1] |= 1u << (r0 + 16 * (i & 1));
+      } else {
+        atomicOr(&d.hdr->err, kErrIndex);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint4 ol, oh;
+    turn_row<false>(xl[i], xh[i], t, 1.f, ol, oh, most);
+    put_row(tile, r0 + 16 * i, ch, ol, oh);
+    t.advance(step);
+  }
+  __shared__ uint32_t words[4];
+  if (lt < 4) words[lt] = 0u;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    if (ch == 0) atomicOr(&words[w], word[w]);
+  __syncthreads();
+  if (lt == 0) a.live[blockIdx.x] = make_uint4(words[0], words[1], words[2], words[3]);
+  if (beyond_half(most))  // any of the head's items may read this tile
+    for (int tile_i = 0; tile_i < d.tiles; ++tile_i) redo_mark(a, hl * d.tiles + tile_i) = 1u;
+}
+
+// One bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// IMG: keys and queries come rotated, as images (dense_images_kernel); otherwise the loaders
+// rotate them.  Registers a thread: 16 warps launched with 128 give the softmax 192, the loaders
+// 72 and the last four warps 56 (65,536 in all); without images 13 warps launched with 128 give
+// 112, 152 and 128 (52,224 of 53,248).
+template <bool IMG>
+__global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkArgs a) {
+  constexpr int kChunkThreads = IMG ? 512 : 416;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
   const DenseArgs &d = a.d;
@@ -276,7 +385,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
   }
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sm.k_full[i], kLoadThreads);
+      mbar_init(&sm.k_full[i], IMG ? 1 : kLoadThreads);
       mbar_init(&sm.v_full[i], kLoadThreads);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_empty[i], 1);
@@ -328,6 +437,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax and epilogue
+    if constexpr (IMG)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t ts = tmem + lanes + t * kTile, to = tmem + lanes + 2 * kTile + t * kTile;
@@ -351,28 +464,50 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
         umma::fence_after_sync();
         uint32_t live[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < (IMG ? 1 : 4); ++w) {
           const uint4 lv = *reinterpret_cast<const uint4 *>(sm.live[n_tile & 3][w]);
           live[0] |= lv.x, live[1] |= lv.y, live[2] |= lv.z, live[3] |= lv.w;
         }
         const bool whole = a0 <= 0 && a1 >= kTile && (live[0] & live[1] & live[2] & live[3]) == 0xffffffffu;
         const bool masked = __any_sync(0xffffffffu, !whole);
         float x = -INFINITY;
+        [[maybe_unused]] uint32_t sr[IMG ? 4 : 1][32];  // the row's scores
+        if constexpr (IMG) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t s[32];
-          umma::tmem_ld32(ts + g * 32, s);
+          for (int g = 0; g < 4; ++g) umma::tmem_ld32(ts + g * 32, sr[g]);
           umma::tmem_wait_ld();
           if (masked) {
-            const uint32_t w = live[g];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = g * 32 + i;
-              if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
-            }
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int c = g * 32 + i;
+                if (c < a0 || c >= a1 || !((live[g] >> i) & 1u)) sr[g][i] = 0xff800000u;
+              }
           }
+          float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x = fmaxf(x, __uint_as_float(s[i]));
+          for (int i = 0; i < 32; i += 2)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) xs[g] = max3(xs[g], __uint_as_float(sr[g][i]), __uint_as_float(sr[g][i + 1]));
+          x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3]));
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t s[32];
+            umma::tmem_ld32(ts + g * 32, s);
+            umma::tmem_wait_ld();
+            if (masked) {
+              const uint32_t w = live[g];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int c = g * 32 + i;
+                if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) x = max3(x, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          }
         }
         const bool up = x > m + kRescale || (m == -INFINITY && x > m);
         if (__any_sync(0xffffffffu, up)) {
@@ -395,31 +530,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
           }
         }
         const float z = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        const F2 nz = f2(-z, -z);
+        F2 sum = f2(0.f, 0.f);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t s[32], pk[16];
-          umma::tmem_ld32(ts + g * 32, s);
-          umma::tmem_wait_ld();
-          if (masked) {
-            const uint32_t w = live[g];
+          if constexpr (IMG) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = g * 32 + i;
-              if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
+            for (int i = 0; i < 32; ++i) s[i] = sr[g][i];
+          } else {
+            umma::tmem_ld32(ts + g * 32, s);
+            umma::tmem_wait_ld();
+            if (masked) {
+              const uint32_t w = live[g];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int c = g * 32 + i;
+                if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
+              }
             }
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float e0 = exp2_approx(__uint_as_float(s[2 * i]) - z);
-            const float e1 = exp2_approx(__uint_as_float(s[2 * i + 1]) - z);
-            l0 += e0;
-            l1 += e1;
+            const float2 x2 = f2_get(f2_add(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), nz));
+            const float e0 = exp2_approx(x2.x), e1 = exp2_approx(x2.y);
+            sum = f2_add(sum, f2(e0, e1));
             pk[i] = cvt_bf16x2(e0, e1);
           }
           tmem_st16(ts + g * 16, pk);  // over columns that were read
         }
-        l += l0 + l1;
+        l += f2_get(sum).x + f2_get(sum).y;
         tmem_wait_st();
         umma::fence_before_sync();
         __syncwarp();
@@ -523,71 +663,113 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
           }
         }
       }
-      if (odd && in) a.redo[sg.item % kMaxShared] = 1u;
+      if (odd && in) redo_mark(a, sg.item) = 1u;
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ loaders
+    if constexpr (IMG)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int lt = tid - kSoftWarps * 32, ch = lt & 7;
     const uint64_t *f = ws_freq(d.hdr) + ch * 8;
-    Turn step;
-    step.set(f, 16);
+    const int r0 = lt >> 3;  // this thread's rows: r0 + 16 i
+    [[maybe_unused]] Turn step, t;
+    if constexpr (!IMG) step.set(f, 16);
     uint32_t n = 0;  // key tiles loaded
     bool ok = true;
     while (ok && segments_next(a, sm, sg, it)) {
       __half2 most = __floats2half2_rn(0.f, 0.f);
-      for (int j = sg.j0; j < sg.j1; ++j, ++n) {
+      // Rows of key tile j in the caches (fewer than 2^32 rows fit a GPU); bit i of the result:
+      // this thread's row i is a token of the range on a page of the pool.
+      uint32_t rows[8], here;
+      auto place = [&](int j) {
         const bool sink = j < it.n1;
         const int T = (sink ? j : it.first + j - it.n1) * kTile;
         const int lo = sink ? 0 : it.lo2, hi = sink ? it.hi1 : it.hi2;
+        here = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = T + r0 + 16 * i;
+          rows[i] = 0;
+          if (tok >= lo && tok < hi) {
+            const int64_t r = cache_row(d, it.b, it.h, tok);
+            if (r >= 0) {
+              rows[i] = (uint32_t)r;
+              here |= 1u << i;
+            } else if (!IMG) {
+              atomicOr(&d.hdr->err, kErrIndex);
+            }
+          }
+        }
+      };
+      [[maybe_unused]] uint4 xl[2][4], xh[2][4];  // raw keys of half a tile, the next half in flight while one is turned
+      auto fetch = [&](int hf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool on = (here >> (hf * 4 + i)) & 1u;
+          const uint4 *src = reinterpret_cast<const uint4 *>(d.k + (int64_t)rows[hf * 4 + i] * kD);
+          xl[hf][i] = on ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+          xh[hf][i] = on ? __ldg(src + ch + 8) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto turn = [&](int hf, int s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 ol, oh;
+          turn_row<false>(xl[hf][i], xh[hf][i], t, 1.f, ol, oh, most);
+          put_row(sm.k[s], r0 + 16 * (hf * 4 + i), ch, ol, oh);
+          t.advance(step);
+        }
+      };
+      place(sg.j0);
+      if constexpr (!IMG) fetch(0);
+      for (int j = sg.j0; j < sg.j1; ++j, ++n) {
+        const bool sink = j < it.n1;
         const int s = n % kRing;
         const uint32_t round = n / kRing;
-        if (j == sg.j0 || (j == it.n1 && j > 0)) {
+        if (!IMG && (j == sg.j0 || (j == it.n1 && j > 0))) {
           // the queries of a new segment, or of the window after the sinks: the products that
           // read the last ones are done once the previous key tile is free
           if (n > 0 && !wait_or_stop(sm, a, &sm.k_empty[(n - 1) % kRing], ((n - 1) / kRing) & 1)) {
             ok = false;
             break;
           }
-          load_queries(a, sm, it, sink, lt, most);
+          load_queries(a, sm.q[0], it, sink, lt, most);
         }
-        // rows of the tile: a token's page is looked up once, by the 8 threads of its row
-        Turn t;
-        t.set(f, T + (lt >> 3));
+        // The rotation goes on from tile to tile (16 positions a row, 128 a tile) and starts anew
+        // every 16 tiles: 128 steps of fp32 rounding are below 2^-16, fp16 rounds at 2^-11.
+        if (!IMG && (j == sg.j0 || j == it.n1 || ((j - sg.j0) & 15) == 0))
+          t.set(f, (sink ? j : it.first + j - it.n1) * kTile + r0);
         if (round > 0 && !wait_or_stop(sm, a, &sm.v_empty[s], (round - 1) & 1)) {
           ok = false;
           break;
         }
-        int64_t rows[8];
-        uint32_t here = 0;  // bit i: this thread's row i is loaded
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int tok = T + (lt >> 3) + 16 * i;
-          rows[i] = 0;
-          if (tok >= lo && tok < hi) {
-            const int64_t r = cache_row(d, it.b, it.h, tok);
-            if (r >= 0) {
-              rows[i] = r;
-              here |= 1u << i;
-            } else {
-              atomicOr(&d.hdr->err, kErrIndex);
-            }
-          }
-          const uint32_t dst = smem_u32(sm.v[s]) + ((lt >> 3) + 16 * i) * 128 + ((ch ^ ((lt >> 3) & 7)) << 4);
+          const uint32_t dst = smem_u32(sm.v[s]) + (r0 + 16 * i) * 128 + ((ch ^ (r0 & 7)) << 4);
           const bool on = (here >> i) & 1u;
-          cp_async16(dst, d.v + rows[i] * kD + ch * 8, on);
-          cp_async16(dst + kHalfBytes, d.v + rows[i] * kD + kHalf + ch * 8, on);
+          const uint16_t *src = d.v + (int64_t)rows[i] * kD + ch * 8;
+          cp_async16(dst, src, on);
+          cp_async16(dst + kHalfBytes, src + kHalf, on);
         }
         cp_async_commit();
+        if constexpr (IMG) {
+          if (j + 1 < sg.j1) place(j + 1);
+          cp_async_wait<0>();
+          umma::fence_async_smem();
+          mbar_arrive(&sm.v_full[s]);
+          continue;
+        }
+        fetch(1);
         if (round > 0 && !wait_or_stop(sm, a, &sm.k_empty[s], (round - 1) & 1)) {
           ok = false;
           break;
         }
-        // live tokens: thread row r = lt / 8 holds tokens r + 16 i; word w of the tile is tokens 32 w ..
-        {
+        {  // live tokens, each warp its rows: word w of the tile is tokens 32 w .. 32 w + 31
           uint32_t word[4] = {0u, 0u, 0u, 0u};
-          const int r = lt >> 3;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) word[i >> 1] |= ((here >> i) & 1u) << (r + 16 * (i & 1));
+          for (int i = 0; i < 8; ++i) word[i >> 1] |= ((here >> i) & 1u) << (r0 + 16 * (i & 1));
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             word[w] |= __shfl_xor_sync(0xffffffffu, word[w], 8);
@@ -596,34 +778,60 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
           if (lane == 0)
             *reinterpret_cast<uint4 *>(sm.live[n & 3][warp - kSoftWarps]) = make_uint4(word[0], word[1], word[2], word[3]);
         }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint4 xl[4], xh[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool on = (here >> (hf * 4 + i)) & 1u;
-            const uint4 *src = reinterpret_cast<const uint4 *>(d.k + rows[hf * 4 + i] * kD);
-            xl[i] = on ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
-            xh[i] = on ? __ldg(src + ch + 8) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 ol, oh;
-            turn_row(xl[i], xh[i], t, 1.f, ol, oh, most);
-            put_row(sm.k[s], (lt >> 3) + 16 * (hf * 4 + i), ch, ol, oh);
-            t.advance(step);
-          }
+        turn(0, s);
+        if (j + 1 < sg.j1) {
+          place(j + 1);
+          fetch(0);
         }
+        turn(1, s);
         umma::fence_async_smem();
         mbar_arrive(&sm.k_full[s]);
         cp_async_wait<0>();
         umma::fence_async_smem();
         mbar_arrive(&sm.v_full[s]);
       }
-      if (__hgt(__hmax(__low2half(most), __high2half(most)), __float2half(65504.f))) a.redo[sg.item % kMaxShared] = 1u;
+      if (!IMG && beyond_half(most)) redo_mark(a, sg.item) = 1u;
     }
     cp_async_wait<0>();
-  } else if (lane == 0) {
+  } else {
+    if constexpr (IMG) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (IMG && warp == 13 && lane == 0) {
+      // ---------------------------------------------------------------- images
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && segments_next(a, sm, sg, it)) {
+        const HeadRange hr = head_range(d, it.len);
+        const int hl = it.b * d.hkv + it.h - a.bh0;
+        for (int j = sg.j0; j < sg.j1; ++j, ++n) {
+          const bool sink = j < it.n1;
+          const int s = n % kRing;
+          const int kt = min(sink ? j : hr.n1 + it.first + j - it.n1 - hr.first, a.key_tiles - 1);
+          const int64_t image = (int64_t)hl * a.key_tiles + kt;
+          const bool queries = j == sg.j0 || (j == it.n1 && j > 0);
+          // new queries: the products that read the last ones are done once the previous tile is free
+          if (queries && n > 0 && !wait_or_stop(sm, a, &sm.k_empty[(n - 1) % kRing], ((n - 1) / kRing) & 1)) {
+            ok = false;
+            break;
+          }
+          if (n >= kRing && !wait_or_stop(sm, a, &sm.k_empty[s], (n / kRing - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          *reinterpret_cast<uint4 *>(sm.live[n & 3][0]) = __ldg(a.live + image);
+          mbar_expect(&sm.k_full[s], kTileBytes + (queries ? 2 * kTileBytes : 0));
+          if (queries)
+            bulk_load(smem_u32(sm.q[0]),
+                      a.query_images + ((int64_t)sg.item * a.query_sets + (sink ? 1 : 0)) * (2 * kTileBytes),
+                      2 * kTileBytes, &sm.k_full[s]);
+          bulk_load(smem_u32(sm.k[s]), a.key_images + image * kTileBytes, kTileBytes, &sm.k_full[s]);
+        }
+      }
+      // every copy has landed before the block may end
+      if (n > 0) mbar_wait(&sm.k_full[(n - 1) % kRing], ((n - 1) / kRing) & 1);
+      if (n > 1) mbar_wait(&sm.k_full[(n - 2) % kRing], ((n - 2) / kRing) & 1);
+    }
+  }
+  if (warp == 12 && lane == 0) {
     // ------------------------------------------------------------------ products
     uint32_t n = 0;         // key tiles
     uint32_t n_p = 0;       // phases of p_full
@@ -693,28 +901,69 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
 
 }  // namespace
 
-int launch_dense_chunk(const DenseArgs &d, int64_t max_keys, void *stream) {
-  ChunkArgs a;
+namespace {
+
+template <bool IMG>
+int run_chunk(const ChunkArgs &a, int64_t tiles, void *stream) {
+  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
+  cudaError_t e = cudaFuncSetAttribute(dense_chunk_kernel<IMG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kChunkSmem);
+  if (e != cudaSuccess) return (int)e;
+  const int64_t work = a.shared ? a.items * tiles : a.items;
+  dense_chunk_kernel<IMG><<<(unsigned)std::min<int64_t>(work, sms), IMG ? 512 : 416, kChunkSmem, (cudaStream_t)stream>>>(a);
+  return (int)cudaGetLastError();
+}
+
+// The most key tiles a head's queries see.
+int64_t most_key_tiles(const DenseArgs &d) {
+  const int64_t all = ceil_div(std::max(d.length, 1), kTile);
+  if (!d.window) return all;
+  return std::min<int64_t>(all, ceil_div((int64_t)d.window + (d.causal ? d.nq : 0), kTile) + 1) +
+         std::min<int64_t>(all, ceil_div(d.sinks, kTile));
+}
+
+}  // namespace
+
+int launch_dense_chunk(const DenseArgs &d, int64_t max_keys, int64_t image_bytes, void *stream) {
+  ChunkArgs a = {};
   a.d = d;
   const int per = kItemRows >> d.group_shift;
   a.d.tiles = (d.nq + per - 1) / per;
-  const int64_t items = (int64_t)d.batch * d.hkv * a.d.tiles;
-  a.items = (int)items;
-  a.redo = nullptr;
-  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
-  // Dealing the key tiles out evenly costs a part's write and join (about four key tiles'
-  // time) and saves the last wave's idle blocks.
-  const int64_t tiles = ceil_div(max_keys, kTile) + 1;
-  const int64_t plain = ceil_div(items, sms) * tiles, dealt = ceil_div(items * tiles, sms) + 4;
-  a.shared = items <= kMaxShared && dealt < plain ? 1 : 0;
+  const int64_t heads = (int64_t)d.batch * d.hkv;
   a.redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(d.hdr) + kDenseRedo);
-  cudaError_t e = cudaFuncSetAttribute(dense_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kChunkSmem);
-  if (e != cudaSuccess) return (int)e;
-  const int64_t work = a.shared ? items * tiles : items;
-  dense_chunk_kernel<<<(unsigned)std::min<int64_t>(work, sms), kChunkThreads, kChunkSmem, (cudaStream_t)stream>>>(a);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? (int)e : launch_dense_redo(d, a.d.tiles, stream);
+  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
+  const int64_t tiles = ceil_div(max_keys, kTile) + 1;
+  // Rotated images pay once two items share a key tile; as many heads a launch as they fit.
+  a.key_tiles = (int)most_key_tiles(d);
+  a.query_sets = d.window && d.sinks && d.rank_sinks ? 2 : 1;
+  const int64_t head_bytes = a.key_tiles * (int64_t)(kTileBytes + sizeof(uint4)) +
+                             (int64_t)a.d.tiles * a.query_sets * 2 * kTileBytes;
+  const int64_t fit = image_bytes / head_bytes;
+  const bool images = a.d.tiles >= kImageTiles && fit >= 1;
+  const int64_t step = images ? std::min(heads, fit) : heads;
+  for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
+    a.bh0 = (int)bh0;
+    a.heads = (int)std::min(step, heads - bh0);
+    a.items = a.heads * a.d.tiles;
+    // Dealing the key tiles out evenly costs a part's write and join (about four key tiles'
+    // time) and saves the last wave's idle blocks.
+    const int64_t plain = ceil_div(a.items, sms) * tiles, dealt = ceil_div(a.items * tiles, sms) + 4;
+    a.shared = a.items <= kMaxShared && dealt < plain ? 1 : 0;
+    int rc;
+    if (images) {
+      a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
+      a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kTileBytes;
+      a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.items * a.query_sets * 2 * kTileBytes);
+      dense_images_kernel<<<(unsigned)(a.heads * a.key_tiles + a.items * a.query_sets), kLoadThreads, 0,
+                            (cudaStream_t)stream>>>(a);
+      rc = (int)cudaGetLastError();
+      if (rc == 0) rc = run_chunk<true>(a, tiles, stream);
+    } else {
+      rc = run_chunk<false>(a, tiles, stream);
+    }
+    if (rc) return rc;
+  }
+  return launch_dense_redo(d, a.d.tiles, stream);
 }
 
 }  // namespace recsa

@@ -21,7 +21,8 @@ constexpr size_t kDensePart = kDenseRedo + kMaxShared * sizeof(uint32_t);  // pa
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
 constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call
-constexpr size_t kDenseBytes = kDenseLse + kMaxDenseLse * sizeof(float);
+constexpr size_t kDenseImages = kDenseLse + kMaxDenseLse * sizeof(float);   // rotated rows of a chunk's keys and queries
+constexpr size_t kMaxDenseImages = (size_t)320 << 20;
 constexpr int kPartRow = kD + 4;  // floats of a row's partial result: maximum, sum, 2 unused, 128 sums
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,7 +49,7 @@ int dense_sm_count();  // of the current device
 int launch_dense_init(void *ws, double base, void *stream);
 int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, void *stream);
 // The chunk kernel (bf16 output), then the rows kernel for the items it marked.
-int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, void *stream);
+int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, int64_t image_bytes, void *stream);
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
 int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
