@@ -13,131 +13,143 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;                  // query rows of a tile: queries x heads of a KV group
 constexpr int kStep = 16;                  // keys of a step
-constexpr int kStages = 2;                 // steps in flight of a warp
 constexpr int kStepBytes = kStep * kRowBytes;
 constexpr int kTableStride = kHalf * 8 + 64;  // bytes of a table row in shared memory
-constexpr int kQStride = kD + 8;              // floats of a query row in shared memory
+constexpr int kQStride = kD + 4;              // floats of a query row in shared memory
+constexpr int kOStride = kD + 8;              // floats of an output row in shared memory
+constexpr float kRowsRescale = 64.f;          // a row's maximum may lag by 2^64 before its output is rescaled
 
+template <int R>  // query rows of a tile: queries x heads of a KV group
 struct RowsSmem {
-  unsigned char stage[kWarps][kStages][2][kStepBytes];  // [K, V]
-  unsigned char table[kSpan * kTableStride];
-  float q[2][kRows][kQStride];         // [window, sinks], scaled, turned to the tile's base position
-  float4 ang[kWarps][kHalf / 2];       // a warp's rotation of the query rows, two frequencies each
-  float m[kWarps][kRows], l[kWarps][kRows];
-  uint32_t live[kWarps][kStages];      // a step's keys that were loaded
-  int pos[kRows];                      // a row's position; 0 or less: nothing visible
+  unsigned char stage[kWarps][2][kStepBytes];  // [K, V]
+  unsigned char table[kSpan * kTableStride];   // two frequencies: cos, cos', sin, sin'
+  float q[2][R][kQStride];             // [window, sinks], scaled, turned to the tile's base position
+  float4 ang[kWarps][kHalf / 2];       // a warp's rotation of the query rows, as the table
+  float m[kWarps][R], l[kWarps][R];
+  int pos[R];                          // a row's position; 0 or less: nothing visible
   int last;
 };
 
-// One step's loads: 16 keys from token T, those outside [lo, hi) or on a page outside the
-// pool as zeros.
-template <bool PV>
-__device__ __forceinline__ uint32_t load_step(const DenseArgs &a, int b, int h, int T, int lo, int hi,
-                                              unsigned char (*st)[kStepBytes], int lane) {
+// One step's rows: 16 keys from token T, those outside [lo, hi) or on a page outside the pool as
+// zeros.  A lane places the row of key lane % 16; `live` are the keys that are there.
+struct Step {
+  int64_t row;
+  uint32_t live;
+};
+__device__ __forceinline__ Step place_step(const DenseArgs &a, int b, int h, int T, int lo, int hi, int lane) {
   const int t = T + (lane & 15);
-  bool live = t >= lo && t < hi;
-  int64_t row = 0;
-  if (live) {
-    row = cache_row(a, b, h, t);
-    if (row < 0) {
-      row = 0;
-      live = false;
+  Step s;
+  bool on = t >= lo && t < hi;
+  s.row = 0;
+  if (on) {
+    s.row = cache_row(a, b, h, t);
+    if (s.row < 0) {
+      s.row = 0;
+      on = false;
       atomicOr(&a.hdr->err, kErrIndex);
     }
   }
-  const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
-  const uint32_t sk = smem_u32(st[0]), sv = smem_u32(st[1]);
+  s.live = __ballot_sync(0xffffffffu, on) & 0xffffu;
+  return s;
+}
+__device__ __forceinline__ void load_step(const uint16_t *cache, const Step &s, uint32_t dst, int lane) {
   const int c = lane & 15;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int key = 2 * i + (lane >> 4);
-    const int64_t r = __shfl_sync(0xffffffffu, row, key);
-    const bool on = (mask >> key) & 1u;
-    const uint32_t off = key * kRowBytes + ((c ^ (key & 7)) << 4);
-    cp_async16(sk + off, a.k + r * kD + c * 8, on);
-    if (PV) cp_async16(sv + off, a.v + r * kD + c * 8, on);
+    const int64_t r = __shfl_sync(0xffffffffu, s.row, key);
+    cp_async16(dst + key * kRowBytes + ((c ^ (key & 7)) << 4), cache + r * kD + c * 8, (s.live >> key) & 1u);
   }
-  return mask;
+  cp_async_commit();
 }
 
-// The tile's rows turned to base position + delta, as the A operands of the score product:
-// q (and with SPLIT what the rounding to bf16 leaves) for this thread's rows lane/4, lane/4+8.
-template <bool SPLIT>
+// 8 query rows turned by a further `delta` positions, as the B operands of the score product: each
+// value as two bf16 parts (q rounded, and what that leaves, rounded).
+template <int NR>
 __device__ __forceinline__ void turn_queries(const DenseArgs &a, const float (*q)[kQStride], int delta, float4 *ang,
-                                             uint32_t (&qh)[8][4], uint32_t (&ql)[SPLIT ? 8 : 1][4], int lane) {
+                                             uint32_t (&qh)[NR][16], uint32_t (&ql)[NR][16], int lane) {
   const uint64_t *f = ws_freq(a.hdr);
   __syncwarp();
   const float2 r0 = rotation(delta, __ldg(f + 2 * lane)), r1 = rotation(delta, __ldg(f + 2 * lane + 1));
-  ang[lane] = make_float4(r0.x, r0.y, r1.x, r1.y);
+  ang[lane] = make_float4(r0.x, r1.x, r0.y, r1.y);
   __syncwarp();
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int ch = 0; ch < 8; ++ch) {  // 8 dimensions: 16 of a k-step are two of these
+  for (int ch = 0; ch < 8; ++ch) {
     const float4 w = ang[ch * 4 + c];
+    const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w);
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-      const float2 x = *reinterpret_cast<const float2 *>(&q[r + 8 * rr][ch * 8 + 2 * c]);
-      const float2 y = *reinterpret_cast<const float2 *>(&q[r + 8 * rr][ch * 8 + 2 * c + kHalf]);
-      const float x0 = x.x * w.x - y.x * w.y, x1 = x.y * w.z - y.y * w.w;
-      const float y0 = y.x * w.x + x.x * w.y, y1 = y.y * w.z + x.y * w.w;
-      const int ks = ch >> 1, reg = (ch & 1) * 2 + rr;
-      qh[ks][reg] = cvt_bf16x2(x0, x1);
-      qh[ks + 4][reg] = cvt_bf16x2(y0, y1);
-      if (SPLIT) {
-        ql[ks][reg] = residue_bf16x2(x0, x1, qh[ks][reg]);
-        ql[ks + 4][reg] = residue_bf16x2(y0, y1, qh[ks + 4][reg]);
-      }
+    for (int nt = 0; nt < NR; ++nt) {
+      const float2 x = *reinterpret_cast<const float2 *>(&q[nt * 8 + r][ch * 8 + 2 * c]);
+      const float2 y = *reinterpret_cast<const float2 *>(&q[nt * 8 + r][ch * 8 + 2 * c + kHalf]);
+      const F2 X = f2(x.x, x.y), Y = f2(y.x, y.y);
+      const float2 u = f2_get(f2_fma(Y, f2_neg(sn), f2_mul(X, cs))), v = f2_get(f2_fma(X, sn, f2_mul(Y, cs)));
+      qh[nt][ch] = cvt_bf16x2(u.x, u.y);
+      qh[nt][ch + 8] = cvt_bf16x2(v.x, v.y);
+      ql[nt][ch] = residue_bf16x2(u.x, u.y, qh[nt][ch]);
+      ql[nt][ch + 8] = residue_bf16x2(v.x, v.y, qh[nt][ch + 8]);
     }
   }
 }
 
-// Scores of the step's keys 8 nt .. 8 nt + 7: rotates them by their place in the span and
-// multiplies.  With SPLIT both operands are two bf16 parts, hi * hi + lo * hi + hi * lo: what
-// is dropped is below 2^-16 of the product of the magnitudes.
-template <bool SPLIT>
-__device__ __forceinline__ void score_keys(const unsigned char *table, uint32_t sk, int T, int nt,
-                                           const uint32_t (&qh)[8][4], const uint32_t (&ql)[SPLIT ? 8 : 1][4],
-                                           float (&s)[4], int lane) {
-  uint32_t kr[16];
-  const int key = nt * 8 + (lane & 7);
+// Scores of a step's 16 keys (rows of the product) with the tile's query rows (columns): the keys
+// are rotated by their place in the span.  Both operands are two bf16 parts, hi * hi + lo * hi +
+// hi * lo: what is dropped is below 2^-16 of the product of the magnitudes.
+// s[nt]: keys lane/4 (first two) and lane/4 + 8, query rows nt * 8 + 2 (lane % 4) and one more.
+template <int NR>
+__device__ __forceinline__ void score_step(const unsigned char *table, uint32_t sk, int T, const uint32_t (&qh)[NR][16],
+                                           const uint32_t (&ql)[NR][16], float (&s)[NR][4], int lane) {
+  const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: lanes 0-15 the first 8 dimensions' rows, 16-31 the next 8
+  const uint32_t lbase = sk + lrow * kRowBytes;
+  const unsigned char *tr = table + ((T & (kSpan - 1)) + (lane >> 2)) * kTableStride + (lane & 3) * 16;
+  float lo[NR][4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    ldsm4(sk + key * kRowBytes + (((4 * g + (lane >> 3)) ^ (key & 7)) << 4), kr[4 * g], kr[4 * g + 1], kr[4 * g + 2],
-          kr[4 * g + 3]);
-  const unsigned char *tr = table + ((T & (kSpan - 1)) + nt * 8 + (lane >> 2)) * kTableStride + (lane & 3) * 16;
-  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[nt][i] = lo[nt][i] = 0.f;
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    uint32_t kh[4], kl[4];  // k-step ks: 0, 1; k-step ks + 4: 2, 3
+    uint32_t x[4], y[4];  // [key half][chunk of the k-step]: registers 0: (0, 0), 1: (1, 0), 2: (0, 1), 3: (1, 1)
+    ldsm4(lbase + (((2 * ks + lch) ^ (lrow & 7)) << 4), x[0], x[1], x[2], x[3]);
+    ldsm4(lbase + (((2 * ks + 8 + lch) ^ (lrow & 7)) << 4), y[0], y[1], y[2], y[3]);
+    uint32_t uh[4], ul[4], vh[4], vl[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int ch = 2 * ks + i;
-      const float4 w = *reinterpret_cast<const float4 *>(tr + ch * 64);
-      const float x0 = bf16_lo(kr[ch]), x1 = bf16_hi(kr[ch]), y0 = bf16_lo(kr[ch + 8]), y1 = bf16_hi(kr[ch + 8]);
-      const float u0 = x0 * w.x - y0 * w.y, u1 = x1 * w.z - y1 * w.w;
-      const float v0 = y0 * w.x + x0 * w.y, v1 = y1 * w.z + x1 * w.w;
-      kh[i] = cvt_bf16x2(u0, u1);
-      kh[2 + i] = cvt_bf16x2(v0, v1);
-      if (SPLIT) {
-        kl[i] = residue_bf16x2(u0, u1, kh[i]);
-        kl[2 + i] = residue_bf16x2(v0, v1, kh[2 + i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (2 * ks + (i >> 1)) * 64);
+      const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]);
+      const float2 u = f2_get(f2_fma(Y, f2_neg(sn), f2_mul(X, cs))), v = f2_get(f2_fma(X, sn, f2_mul(Y, cs)));
+      uh[i] = cvt_bf16x2(u.x, u.y);
+      vh[i] = cvt_bf16x2(v.x, v.y);
+      ul[i] = residue_bf16x2(u.x, u.y, uh[i]);
+      vl[i] = residue_bf16x2(v.x, v.y, vh[i]);
     }
-    mma16816(hi, qh[ks], kh[0], kh[1]);
-    if (SPLIT) mma16816(lo, ql[SPLIT ? ks : 0], kh[0], kh[1]);
-    mma16816(hi, qh[ks + 4], kh[2], kh[3]);
-    if (SPLIT) {
-      mma16816(lo, qh[ks], kl[0], kl[1]);
-      mma16816(lo, ql[SPLIT ? ks + 4 : 0], kh[2], kh[3]);
-      mma16816(lo, qh[ks + 4], kl[2], kl[3]);
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+      mma16816(s[nt], uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+      mma16816(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+      mma16816(s[nt], vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+      mma16816(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
+      mma16816(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+      mma16816(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = hi[i] + lo[i];
+  for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[nt][i] += lo[nt][i];
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
+  uint32_t u;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(addr) : "memory");
+  return u;
+}
 __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
   return (bf16x2 & 0x7f80u) == 0x7f80u || (bf16x2 & 0x7f800000u) == 0x7f800000u;
 }
@@ -148,6 +160,8 @@ struct Range {
   int n1, first;  // steps of the sinks; first step of the window
   int hi1, lo2, hi2;
   int total;
+  __device__ __forceinline__ bool sink(int st) const { return st < n1; }
+  __device__ __forceinline__ int token(int st) const { return (st < n1 ? st : first + st - n1) * kStep; }
 };
 __device__ __forceinline__ Range tile_range(const DenseArgs &a, int p_min, int p_max) {
   Range r;
@@ -160,42 +174,81 @@ __device__ __forceinline__ Range tile_range(const DenseArgs &a, int p_min, int p
   return r;
 }
 
-// One tile of 16 query rows (16 / G queries of one sequence and KV group) against one block's
-// share of the keys they see.  Each warp walks its own steps of 16 keys through a private ring
-// of cp.async stages with an online softmax, so warps never wait for one another until their
-// (max, sum, output) are joined at the end; the last block of a tile joins the blocks.  Reading
-// K and V bounds it: at G = 4 a key costs 512 bytes and about 45 issue slots of its SM's ~88.
-// PV: values are weighted and summed; without it the rows' log2-sum-exp goes to `lse`.
-template <bool SPLIT, bool PV>
-__global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, float *lse, const uint32_t *redo, int chunk_tiles) {
+// One tile of 8 NR query rows (queries x heads of a KV group) against one block's share of the keys
+// they see.  Each warp walks its own steps of 16 keys with an online softmax, its keys and values
+// fetched one step ahead with cp.async into memory of its own, so warps never wait for one another
+// until their (max, sum, output) are joined at the end; the last block of a tile joins the blocks.
+// Scores, probabilities and outputs are products of the tensor cores with keys (scores) and
+// dimensions (outputs) as rows and the query rows as columns, so that one to eight rows - a decode
+// step - fill an instruction.  Reading K and V bounds it: a key of 512 bytes costs about 40 issue
+// slots of the ~88 its SM has meanwhile.
+// MODE 0: the output.  MODE 1: the rows' log2-sum-exp to `lse`.  MODE 2: the output of the tiles
+// that the chunk kernel marked in `redo`, if any.
+template <int NR, int MODE>
+__global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
+    dense_rows_kernel(DenseArgs a, int items, float *lse, uint32_t *redo, int chunk_tiles) {
+  constexpr int R = 8 * NR;
+  constexpr bool PV = MODE != 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  RowsSmem &sm = *reinterpret_cast<RowsSmem *>(smem_raw);
+  RowsSmem<R> &sm = *reinterpret_cast<RowsSmem<R> *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t item = blockIdx.x / a.nsplit;
-  const int split = blockIdx.x % a.nsplit;
-  const int tile = item % a.tiles, bh = item / a.tiles;
-  const int b = bh / a.hkv, h = bh % a.hkv;
   const int gs = a.group_shift, G = 1 << gs, hq = a.hkv << gs;
-  const int q0 = tile * (kRows >> gs), nq = min(kRows >> gs, a.nq - q0);  // the tile's queries
   if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) {
     if (tid == 0) atomicOr(&a.hdr->err, kErrWs);
     return;
   }
-  if (redo) {  // only what the chunk kernel marked
-    const int chunk_item = bh * chunk_tiles + chunk_tiles - 1 - q0 / (256 >> gs);
-    if (!redo[chunk_item % kMaxShared]) return;
+  if (MODE == 2) {  // nearly always nothing is marked
+    uint32_t any = 0;
+    for (int i = tid; i < kMaxShared / 4; i += kThreads) {
+      const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(redo) + i);
+      any |= u.x | u.y | u.z | u.w;
+    }
+    if (!__syncthreads_or(any != 0)) return;
   }
+  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads) {
+    const float4 w = __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
+    *reinterpret_cast<float4 *>(sm.table + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16) =
+        make_float4(w.x, w.z, w.y, w.w);
+  }
+  const int r = lane >> 2, c = lane & 3;
+  const uint32_t sk = smem_u32(sm.stage[warp][0]), sv = sk + kStepBytes;
+
+  for (int work = blockIdx.x; work < items * a.nsplit; work += gridDim.x) {
+  const int item = work / a.nsplit, split = work % a.nsplit;
+  const int tile = item % a.tiles, bh = item / a.tiles;
+  const int b = bh / a.hkv, h = bh % a.hkv;
+  const int q0 = tile * (R >> gs), nq = min(R >> gs, a.nq - q0);  // the tile's queries
+  if (MODE == 2 && !redo[redo_slot(bh, chunk_tiles, q0 / (256 >> gs))]) continue;
   const int len = dense_length(a, b, tid == 0 && tile == 0 && split == 0 && h == 0);
   const int p_min = dense_position(a, len, q0), p_max = dense_position(a, len, q0 + nq - 1);
   const Range rg = tile_range(a, p_min, p_max);
   const int base_sink = sink_position(a, p_max);
 
-  if (tid < kRows) sm.pos[tid] = (tid >> gs) < nq ? dense_position(a, len, q0 + (tid >> gs)) : 0;
-  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads)
-    *reinterpret_cast<float4 *>(sm.table + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16) =
-        __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
-  for (int e = tid; e < kRows * kHalf * 2; e += kThreads) {  // query rows, turned to the tile's last position
-    const int i = e % kHalf, row = (e / kHalf) % kRows, sink = e / (kHalf * kRows);
+  // this warp's steps; the first loads are on their way while the query rows are turned
+  const int64_t parts = (int64_t)a.nsplit * kWarps, part = (int64_t)split * kWarps + warp;
+  const int st0 = (int)(rg.total * part / parts), st1 = (int)(rg.total * (part + 1) / parts);
+  auto place = [&](int st) {
+    const bool sink = rg.sink(st);
+    return place_step(a, b, h, rg.token(st), sink ? 0 : rg.lo2, sink ? rg.hi1 : rg.hi2, lane);
+  };
+  // MODE 1 has no values: its keys alternate between the two halves of the stage
+  Step cur = {0, 0u}, next = {0, 0u};
+  if (st0 < st1) {
+    cur = place(st0);
+    load_step(a.k, cur, PV || !(st0 & 1) ? sk : sv, lane);
+    if (PV) load_step(a.v, cur, sv, lane);
+  }
+  if (!PV) {
+    if (st0 + 1 < st1) {
+      next = place(st0 + 1);
+      load_step(a.k, next, st0 & 1 ? sk : sv, lane);
+    } else {
+      cp_async_commit();
+    }
+  }
+  if (tid < R) sm.pos[tid] = (tid >> gs) < nq ? dense_position(a, len, q0 + (tid >> gs)) : 0;
+  for (int e = tid; e < R * kHalf * 2; e += kThreads) {  // query rows, turned to the tile's last position
+    const int i = e % kHalf, row = (e / kHalf) % R, sink = e / (kHalf * R);
     if (sink && !rg.n1) break;
     float x = 0.f, y = 0.f;
     if ((row >> gs) < nq) {
@@ -216,136 +269,141 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, fl
   }
   __syncthreads();
 
-  // this warp's steps
-  const int64_t parts = (int64_t)a.nsplit * kWarps, part = (int64_t)split * kWarps + warp;
-  const int st0 = (int)(rg.total * part / parts), st1 = (int)(rg.total * (part + 1) / parts);
-  auto start = [&](int st) {
-    const int s = st % kStages;
-    const bool sink = st < rg.n1;
-    const int T = (sink ? st : rg.first + st - rg.n1) * kStep;
-    const uint32_t m = load_step<PV>(a, b, h, T, sink ? 0 : rg.lo2, sink ? rg.hi1 : rg.hi2, sm.stage[warp][s], lane);
-    if (lane == 0) sm.live[warp][s] = m;
-  };
-  const int r = lane >> 2, c = lane & 3;
-  const int pa = sm.pos[r], pb = sm.pos[r + 8];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  float o[PV ? 16 : 1][4];
+  // this thread's query rows: nt * 8 + 2 c + i
+  float m[NR][2], l[NR][2], o[PV ? NR : 1][8][4];
+  int p_lo = 0x7fffffff, p_hi = 0;  // the least and largest position of the tile's rows
 #pragma unroll
-  for (int i = 0; i < (PV ? 16 : 1); ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  uint32_t qh[8][4], ql[SPLIT ? 8 : 1][4];
+  for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m[nt][i] = -INFINITY;
+      l[nt][i] = 0.f;
+    }
+    if (PV) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[nt][d][0] = o[nt][d][1] = o[nt][d][2] = o[nt][d][3] = 0.f;
+    }
+  }
+  p_lo = p_min;
+  p_hi = p_max;
+  uint32_t qh[NR][16], ql[NR][16];
   int turned = -1;  // the span the query rows are turned for (sinks: odd)
 
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (st0 + i < st1) start(st0 + i);
-    cp_async_commit();
-  }
   for (int st = st0; st < st1; ++st) {
-    if (st + kStages - 1 < st1) start(st + kStages - 1);
-    cp_async_commit();
-    const bool sink = st < rg.n1;
-    const int T = (sink ? st : rg.first + st - rg.n1) * kStep;
+    const bool sink = rg.sink(st);
+    const int T = rg.token(st);
     const int span = (T / kSpan) * 2 + (sink ? 1 : 0);
     if (span != turned) {
       turned = span;
-      turn_queries<SPLIT>(a, sm.q[sink], (sink ? base_sink : p_max) - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
+      turn_queries<NR>(a, sm.q[sink], (sink ? base_sink : p_max) - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
     }
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<1>();
     __syncwarp();
-    const uint32_t sk = smem_u32(sm.stage[warp][st % kStages][0]), sv = sk + kStepBytes;
-    const uint32_t live = sm.live[warp][st % kStages];
-    // tokens [la, ha) and [lb, hb) are visible to this thread's two rows
-    const int la = sink ? 0 : window_first(a, pa), lb = sink ? 0 : window_first(a, pb);
-    const int ha = sink ? min(pa, rg.hi1) : pa, hb = sink ? min(pb, rg.hi1) : pb;
-    float s[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      score_keys<SPLIT>(sm.table, sk, T, nt, qh, ql, s[nt], lane);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = nt * 8 + 2 * c + i, t = T + j;
-        const bool on = (live >> j) & 1u;
-        if (!(on && t >= la && t < ha)) s[nt][i] = -INFINITY;
-        if (!(on && t >= lb && t < hb)) s[nt][2 + i] = -INFINITY;
-      }
+    float s[NR][4];
+    const uint32_t keys = PV || !(st & 1) ? sk : sv;
+    score_step<NR>(sm.table, keys, T, qh, ql, s, lane);
+    __syncwarp();  // the keys' memory is free
+    const uint32_t live = cur.live;
+    constexpr int kAhead = PV ? 1 : 2;
+    if (!PV) cur = next;
+    if (st + kAhead < st1) {
+      next = place(st + kAhead);
+      load_step(a.k, next, keys, lane);
+    } else {
+      cp_async_commit();
     }
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    // every row sees every key of the step unless it meets an end of some row's range
+    const bool whole = live == 0xffffu && (sink ? T + kStep <= min(p_lo, rg.hi1)
+                                                : T + kStep <= p_lo && T >= window_first(a, p_hi));
+    bool seen[NR][4];
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-    }
-    const bool up = x0 > m0 || x1 > m1;
-    if (__any_sync(0xffffffffu, up)) {
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
-      if (PV) {
+    for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][0] *= f0;
-          o[i][1] *= f0;
-          o[i][2] *= f1;
-          o[i][3] *= f1;
+      for (int i = 0; i < 4; ++i) seen[nt][i] = true;
+    if (!whole) {
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = r + (i & 2) * 4, t = T + key, p = sm.pos[nt * 8 + 2 * c + (i & 1)];
+          const int lo = sink ? 0 : window_first(a, p), hi = sink ? min(p, rg.hi1) : p;
+          seen[nt][i] = ((live >> key) & 1u) && t >= lo && t < hi;
+          if (!seen[nt][i]) s[nt][i] = -INFINITY;
         }
-      }
     }
-    const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-    bool hidden = false;  // some key of the step is not seen by some row of this thread
+    // Weights from the maximum so far: weights, sums and outputs hold numbers up to 2^127 with
+    // the same relative precision.  Only a row whose maximum has grown by more than 2^64 (or that
+    // has none yet) takes a new one.
+    bool up = false;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hidden |= s[nt][i] == -INFINITY || s[nt][2 + i] == -INFINITY;
-        s[nt][i] = exp2_approx(s[nt][i] - z0);
-        s[nt][2 + i] = exp2_approx(s[nt][2 + i] - z1);
-        l0 += s[nt][i];
-        l1 += s[nt][2 + i];
+      for (int i = 0; i < 4; ++i) up |= s[nt][i] > m[nt][i & 1] + kRowsRescale;
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = fmaxf(s[nt][i], s[nt][2 + i]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          if (x > m[nt][i] + kRowsRescale) {
+            const float f = m[nt][i] == -INFINITY ? 0.f : exp2_approx(m[nt][i] - x);
+            m[nt][i] = x;
+            l[nt][i] *= f;
+            if (PV) {
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[nt][d][i] *= f;
+                o[nt][d][2 + i] *= f;
+              }
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float mm = m[nt][i & 1];
+        s[nt][i] = exp2_approx(s[nt][i] - (mm == -INFINITY ? 0.f : mm));
+        l[nt][i & 1] += s[nt][i];
       }
     if (PV) {
+      cp_async_wait<1>();
+      __syncwarp();
       // A row that does not see a key must not touch its value: a product with a zero weight
       // would carry an infinity or NaN over.  In steps that hide a key from some row, values
       // that are not finite go to the rows that see them one by one and are zeros in the product.
-      if (__any_sync(0xffffffffu, hidden)) {
+      if (!whole) {
         bool odd = false;
-        for (int i = lane; i < kStepBytes / 4; i += 32) {
-          uint32_t u;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sv + i * 4));
-          odd |= not_finite(u);
-        }
+        for (int i = lane; i < kStepBytes / 4; i += 32) odd |= not_finite(ld_shared32(sv + i * 4));
         if (__any_sync(0xffffffffu, odd)) {
-          for (int j = 0; j < kStep; ++j) {
-            const int src = (lane & ~3) | ((j & 7) >> 1);
-            const float e0 = (j & 8) ? ((j & 1) ? s[1][1] : s[1][0]) : ((j & 1) ? s[0][1] : s[0][0]);
-            const float e1 = (j & 8) ? ((j & 1) ? s[1][3] : s[1][2]) : ((j & 1) ? s[0][3] : s[0][2]);
-            const float w0 = __shfl_sync(0xffffffffu, e0, src), w1 = __shfl_sync(0xffffffffu, e1, src);
-            const bool on = (live >> j) & 1u;
-            const bool va = on && T + j >= la && T + j < ha, vb = on && T + j >= lb && T + j < hb;
+          for (int key = 0; key < kStep; ++key) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              uint32_t u;
-              asm volatile("ld.shared.u32 %0, [%1];"
-                           : "=r"(u)
-                           : "r"(sv + j * kRowBytes + ((n ^ (j & 7)) << 4) + c * 4));
-              const float v0 = bf16_lo(u), v1 = bf16_hi(u);
-              if (!isfinite(v0)) {
-                if (va) o[PV ? n : 0][0] += w0 * v0;
-                if (vb) o[PV ? n : 0][2] += w1 * v0;
-              }
-              if (!isfinite(v1)) {
-                if (va) o[PV ? n : 0][1] += w0 * v1;
-                if (vb) o[PV ? n : 0][3] += w1 * v1;
-              }
+            for (int nt = 0; nt < NR; ++nt) {
+              // the weights of this key and this thread's rows sit in the lane of key % 8
+              const int src = (key & 7) * 4 + c;
+              const float w0 = __shfl_sync(0xffffffffu, key & 8 ? s[nt][2] : s[nt][0], src);
+              const float w1 = __shfl_sync(0xffffffffu, key & 8 ? s[nt][3] : s[nt][1], src);
+              const bool v0 = __shfl_sync(0xffffffffu, (int)(key & 8 ? seen[nt][2] : seen[nt][0]), src);
+              const bool v1 = __shfl_sync(0xffffffffu, (int)(key & 8 ? seen[nt][3] : seen[nt][1]), src);
+#pragma unroll
+              for (int d = 0; d < 8; ++d)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {  // dimension 16 d + 8 k + r
+                  const uint32_t u = ld_shared32(sv + key * kRowBytes + (((2 * d + k) ^ (key & 7)) << 4) + (r >> 1) * 4);
+                  const float v = (r & 1) ? bf16_hi(u) : bf16_lo(u);
+                  if (!isfinite(v)) {
+                    if (v0) o[PV ? nt : 0][d][2 * k] += w0 * v;
+                    if (v1) o[PV ? nt : 0][d][2 * k + 1] += w1 * v;
+                  }
+                }
             }
           }
           __syncwarp();
           for (int i = lane; i < kStepBytes / 4; i += 32) {
-            uint32_t u;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sv + i * 4));
+            uint32_t u = ld_shared32(sv + i * 4);
             if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
             if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(sv + i * 4), "r"(u) : "memory");
@@ -353,92 +411,101 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, fl
           __syncwarp();
         }
       }
-      {
-        uint32_t ph[4], pl[4];
+      uint32_t ph[NR][2], pl[NR][2];  // the weights with keys along the k of the product
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr) {
-            ph[nt * 2 + rr] = cvt_bf16x2(s[nt][2 * rr], s[nt][2 * rr + 1]);
-            if (SPLIT) pl[nt * 2 + rr] = residue_bf16x2(s[nt][2 * rr], s[nt][2 * rr + 1], ph[nt * 2 + rr]);
-          }
-        const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t hi = cvt_bf16x2(s[nt][2 * k], s[nt][2 * k + 1]);
+          ph[nt][k] = transpose8x8(hi);
+          pl[nt][k] = transpose8x8(residue_bf16x2(s[nt][2 * k], s[nt][2 * k + 1], hi));
+        }
+      const int key = (lane & 7) + ((lane >> 4) << 3), dch = (lane >> 3) & 1;
 #pragma unroll
-        for (int d = 0; d < 16; d += 2) {
-          uint32_t b0, b1, b2, b3;
-          ldsm4_trans(sv + key * kRowBytes + (((d + (lane >> 4)) ^ (key & 7)) << 4), b0, b1, b2, b3);
-          if (SPLIT) {
-            // The tensor cores cut their fp32 sums off instead of rounding them: over a million
-            // keys an output summed there alone came out 5e-5 short.  A step's 16 keys are
-            // summed there, the steps in fp32 adds that round.
-            float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(t0, pl, b0, b1);
-            mma16816(t1, pl, b2, b3);
-            mma16816(t0, ph, b0, b1);
-            mma16816(t1, ph, b2, b3);
+      for (int d = 0; d < 8; ++d) {
+        uint32_t v[4];
+        ldsm4_trans(sv + key * kRowBytes + (((2 * d + dch) ^ (key & 7)) << 4), v[0], v[1], v[2], v[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[PV ? d : 0][i] += t0[i];
-              o[PV ? d + 1 : 0][i] += t1[i];
-            }
-          } else {
-            mma16816(o[PV ? d : 0], ph, b0, b1);
-            mma16816(o[PV ? d + 1 : 0], ph, b2, b3);
-          }
+        for (int nt = 0; nt < NR; ++nt) {
+          // The tensor cores cut their fp32 sums off instead of rounding them: over a million
+          // keys an output summed there alone came out 5e-5 short.  A step's 16 keys are
+          // summed there, the steps in fp32 adds that round.
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(t, v, pl[nt][0], pl[nt][1]);
+          mma16816(t, v, ph[nt][0], ph[nt][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[PV ? nt : 0][d][i] += t[i];
         }
       }
+      __syncwarp();  // the values' memory is free
+      if (st + 1 < st1)
+        load_step(a.v, next, sv, lane);
+      else
+        cp_async_commit();
     }
-    __syncwarp();  // the stage is free for the next load
+    if (PV) cur = next;
   }
   cp_async_wait<0>();
 
   // join the warps: their outputs in the stage memory
 #pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-  }
-  if (c == 0) {
-    sm.m[warp][r] = m0;
-    sm.m[warp][r + 8] = m1;
-    sm.l[warp][r] = l0;
-    sm.l[warp][r + 8] = l1;
-  }
-  __syncthreads();
-  float *const wo = reinterpret_cast<float *>(sm.stage);  // [warp][16][kQStride]
-  if (PV) {
+  for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-    for (int n = 0; n < 16; ++n) {
-      float *p = wo + (warp * kRows + r) * kQStride + n * 8 + 2 * c;
-      *reinterpret_cast<float2 *>(p) = make_float2(o[PV ? n : 0][0], o[PV ? n : 0][1]);
-      *reinterpret_cast<float2 *>(p + 8 * kQStride) = make_float2(o[PV ? n : 0][2], o[PV ? n : 0][3]);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+      if (r == 0) {
+        sm.m[warp][nt * 8 + 2 * c + i] = m[nt][i];
+        sm.l[warp][nt * 8 + 2 * c + i] = l[nt][i];
+      }
     }
-  }
   __syncthreads();
-  const int row = tid >> 4, d0 = (tid & 15) * 8;  // a thread: 8 dimensions of a row
-  float m = -INFINITY, l = 0.f, acc[8] = {};
+  float *const wo = reinterpret_cast<float *>(sm.stage);  // [warp][R][kOStride], half the warps at a time
+  static_assert(sizeof(float) * (kWarps / NR) * R * kOStride <= sizeof(sm.stage), "the outputs fit the stages");
+  constexpr int kPer = kD * R / kThreads;  // dimensions of a row that a thread joins
+  const int row = tid / (kD / kPer), d0 = (tid % (kD / kPer)) * kPer;
+  float mx = -INFINITY, sum = 0.f, acc[kPer] = {};
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][row]);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float mw = sm.m[w][row];
-    if (mw == -INFINITY) continue;
-    const float f = exp2_approx(mw - m);
-    l += f * sm.l[w][row];
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][row]);
+#pragma unroll 1
+  for (int w0 = 0; w0 < kWarps; w0 += kWarps / NR) {
     if (PV) {
-      const float4 *p = reinterpret_cast<const float4 *>(wo + (w * kRows + row) * kQStride + d0);
-      const float4 u = p[0], v = p[1];
-      acc[0] += f * u.x, acc[1] += f * u.y, acc[2] += f * u.z, acc[3] += f * u.w;
-      acc[4] += f * v.x, acc[5] += f * v.y, acc[6] += f * v.z, acc[7] += f * v.w;
+      if (w0 > 0) __syncthreads();
+      if (warp >= w0 && warp < w0 + kWarps / NR) {
+        float *dst = wo + (warp - w0) * R * kOStride + r;
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[(nt * 8 + 2 * c + (i & 1)) * kOStride + d * 16 + (i >> 1) * 8] = o[PV ? nt : 0][d][i];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps / NR; ++w) {
+      const float mw = sm.m[w0 + w][row];
+      if (mw == -INFINITY) continue;
+      const float f = exp2_approx(mw - mx);
+      sum += f * sm.l[w0 + w][row];
+      if (PV) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) {
+          const float4 u = *reinterpret_cast<const float4 *>(wo + (w * R + row) * kOStride + d0 + i);
+          acc[i] += f * u.x, acc[i + 1] += f * u.y, acc[i + 2] += f * u.z, acc[i + 3] += f * u.w;
+        }
+      }
     }
   }
+  bool write = true;
   if (a.nsplit > 1) {  // leave this block's part; the last block of the tile joins them in order
-    float *part_row = ws_part(a.hdr) + ((int64_t)blockIdx.x * kRows + row) * kPartRow;
-    if (d0 == 0) *reinterpret_cast<float2 *>(part_row) = make_float2(m, l);
+    float *part_row = ws_part(a.hdr) + ((int64_t)work * R + row) * kPartRow;
+    if (d0 == 0) *reinterpret_cast<float2 *>(part_row) = make_float2(mx, sum);
     if (PV) {
-      float4 *p = reinterpret_cast<float4 *>(part_row + 4 + d0);
-      p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4)
+        *reinterpret_cast<float4 *>(part_row + 4 + d0 + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     }
     __threadfence();
     __syncthreads();
@@ -448,46 +515,67 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, fl
       if (sm.last) ws_count(a.hdr)[item] = 0;  // for the next call
     }
     __syncthreads();
-    if (!sm.last) return;
-    __threadfence();
-    const float *p0 = ws_part(a.hdr) + ((int64_t)item * a.nsplit * kRows + row) * kPartRow;
-    const int64_t stride = (int64_t)kRows * kPartRow;
-    m = -INFINITY;
-    l = 0.f;
-    for (int j = 0; j < a.nsplit; ++j) m = fmaxf(m, __ldcg(p0 + j * stride));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    write = sm.last;
+    if (write) {
+      __threadfence();
+      const float *p0 = ws_part(a.hdr) + ((int64_t)item * a.nsplit * R + row) * kPartRow;
+      const int64_t stride = (int64_t)R * kPartRow;
+      mx = -INFINITY;
+      sum = 0.f;
 #pragma unroll 4
-    for (int j = 0; j < a.nsplit; ++j) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p0 + j * stride));
-      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-      if (ml.x == -INFINITY) continue;
-      l += f * ml.y;
-      if (PV) {
-        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p0 + j * stride + 4 + d0));
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p0 + j * stride + 8 + d0));
-        acc[0] += f * u.x, acc[1] += f * u.y, acc[2] += f * u.z, acc[3] += f * u.w;
-        acc[4] += f * v.x, acc[5] += f * v.y, acc[6] += f * v.z, acc[7] += f * v.w;
+      for (int j = 0; j < a.nsplit; ++j) mx = fmaxf(mx, __ldcg(p0 + j * stride));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < a.nsplit; ++j) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p0 + j * stride));
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mx);
+        float4 u[kPer / 4];
+        if (PV) {
+#pragma unroll
+          for (int i = 0; i < kPer / 4; ++i) u[i] = __ldcg(reinterpret_cast<const float4 *>(p0 + j * stride + 4 + d0) + i);
+        }
+        if (ml.x == -INFINITY) continue;
+        sum += f * ml.y;
+        if (PV) {
+#pragma unroll
+          for (int i = 0; i < kPer / 4; ++i) {
+            acc[4 * i] += f * u[i].x, acc[4 * i + 1] += f * u[i].y;
+            acc[4 * i + 2] += f * u[i].z, acc[4 * i + 3] += f * u[i].w;
+          }
+        }
       }
     }
   }
-  if ((row >> gs) >= nq) return;
-  const int64_t out_row = ((int64_t)b * a.nq + q0 + (row >> gs)) * hq + h * G + (row & (G - 1));
-  if (!PV) {
-    if (d0 == 0) lse[out_row] = l > 0.f || !(l == l) ? m + log2f(l) : INFINITY;  // no key: every weight is exp2(-inf)
-    return;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (write && (row >> gs) < nq) {
+    const int64_t out_row = ((int64_t)b * a.nq + q0 + (row >> gs)) * hq + h * G + (row & (G - 1));
+    if (!PV) {
+      // no key: every weight is exp2(-inf)
+      if (d0 == 0) lse[out_row] = sum > 0.f || sum != sum ? mx + log2f(sum) : INFINITY;
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] *= inv;
-  if (a.out_fp32) {
-    float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + out_row * kD + d0);
-    p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  } else {
-    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.out) + out_row * kD + d0) =
-        make_uint4(cvt_bf16x2(acc[0], acc[1]), cvt_bf16x2(acc[2], acc[3]), cvt_bf16x2(acc[4], acc[5]),
-                   cvt_bf16x2(acc[6], acc[7]));
+      for (int i = 0; i < kPer; i += 4) {
+        const float x0 = acc[i] * inv, x1 = acc[i + 1] * inv, x2 = acc[i + 2] * inv, x3 = acc[i + 3] * inv;
+        if (a.out_fp32)
+          *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + out_row * kD + d0 + i) =
+              make_float4(x0, x1, x2, x3);
+        else
+          *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + out_row * kD + d0 + i) =
+              make_uint2(cvt_bf16x2(x0, x1), cvt_bf16x2(x2, x3));
+      }
+    }
+  }
+  __syncthreads();  // the shared memory is free for the next tile
+  }
+  if (MODE == 2) {  // the last block to finish clears the marks
+    __syncthreads();
+    if (tid == 0) sm.last = atomicAdd(ws_count(a.hdr) + kMaxShared, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (sm.last) {
+      for (int i = tid; i < kMaxShared; i += kThreads) redo[i] = 0u;
+      if (tid == 0) ws_count(a.hdr)[kMaxShared] = 0;
+    }
   }
 }
 
@@ -498,12 +586,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(DenseArgs a, fl
 // the pass that summed lse formed them.
 
 struct WeightsSmem {
-  unsigned char stage[kWarps][kStep * 2][kRowBytes];  // 32 keys of a warp
+  unsigned char stage[kWarps][2][kStepBytes];  // 32 keys of a warp
   unsigned char table[kSpan * kTableStride];
-  float q[kRows][kQStride];
+  float q[16][kQStride];
   float4 ang[kWarps][kHalf / 2];
-  float lse[kRows];
-  int pos[kRows];
+  float lse[16];
+  int pos[16];
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -519,42 +607,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int len = dense_length(a, b, tid == 0 && split == 0 && h == 0);
-  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads)
+  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads) {
+    const float4 w = __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
     *reinterpret_cast<float4 *>(sm.table + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16) =
-        __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
+        make_float4(w.x, w.z, w.y, w.w);
+  }
   const int steps = (len + 31) / 32;  // 32 keys a warp, 8 warps a round
   const int rounds = (steps + kWarps - 1) / kWarps;
   const int r = lane >> 2, c = lane & 3;
-  const int qt = kRows >> gs;
+  const int qt = 16 >> gs;
   float *const w_row = weights + ((int64_t)b * a.hkv + h) * a.capacity;
 
   for (int rd = split; rd < rounds; rd += a.nsplit) {
     const int T = (rd * kWarps + warp) * 32;
-    uint32_t live = 0;
+    uint32_t live[2];
     __syncwarp();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int Th = T + half * kStep;
-      unsigned char(*st)[kStepBytes] = reinterpret_cast<unsigned char(*)[kStepBytes]>(sm.stage[warp][half * kStep]);
-      live |= load_step<false>(a, b, h, Th, 0, len, st, lane) << (16 * half);
+      const Step st = place_step(a, b, h, T + half * kStep, 0, len, lane);
+      live[half] = st.live;
+      load_step(a.k, st, smem_u32(sm.stage[warp][half]), lane);
     }
-    cp_async_commit();
     cp_async_wait<0>();
     __syncwarp();
-    const uint32_t sk = smem_u32(sm.stage[warp]);
-    float sum[4][2];
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
+    float sum[2][2] = {};  // keys r and r + 8 of each half
     for (int q0 = 0; q0 < a.nq; q0 += qt) {
       const int nq = min(qt, a.nq - q0);
       const int p_max = dense_position(a, len, q0 + nq - 1);
       __syncthreads();
-      if (tid < kRows) {
+      if (tid < 16) {
         const bool in = (tid >> gs) < nq;
         sm.pos[tid] = in ? dense_position(a, len, q0 + (tid >> gs)) : 0;
         sm.lse[tid] = in ? lse[((int64_t)b * a.nq + q0 + (tid >> gs)) * hq + h * G + (tid & (G - 1))] : INFINITY;
       }
-      for (int e = tid; e < kRows * kHalf; e += kThreads) {
+      for (int e = tid; e < 16 * kHalf; e += kThreads) {
         const int i = e % kHalf, row = e / kHalf;
         float x = 0.f, y = 0.f;
         if ((row >> gs) < nq) {
@@ -574,35 +660,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncthreads();
       if (T < len && p_max > T) {
-        uint32_t qh[8][4], ql[8][4];
-        turn_queries<true>(a, sm.q, p_max - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
-        const int pa = sm.pos[r], pb = sm.pos[r + 8];
-        const float za = sm.lse[r], zb = sm.lse[r + 8];
+        uint32_t qh[2][16], ql[2][16];
+        turn_queries<2>(a, sm.q, p_max - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          float s[4];
-          score_keys<true>(sm.table, sk, T, nt, qh, ql, s, lane);
+        for (int half = 0; half < 2; ++half) {
+          float s[2][4];
+          const int Th = T + half * kStep;
+          score_step<2>(sm.table, smem_u32(sm.stage[warp][half]), Th, qh, ql, s, lane);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = T + nt * 8 + 2 * c + i;
-            if (t < pa) sum[nt][i] += exp2_approx(s[i] - za);
-            if (t < pb) sum[nt][i] += exp2_approx(s[2 + i] - zb);
-          }
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = nt * 8 + 2 * c + (i & 1);
+              if (Th + r + (i & 2) * 4 < sm.pos[row]) sum[half][i >> 1] += exp2_approx(s[nt][i] - sm.lse[row]);
+            }
         }
       }
     }
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v = sum[nt][i];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        const int j = nt * 8 + 2 * c + i;
-        if (r == 0 && T + j < len) {
-          if (!((live >> j) & 1u)) v = 0.f;  // a token on a page outside the pool receives nothing
-          w_row[T + j] = accumulate ? w_row[T + j] + v : v;
+      for (int k = 0; k < 2; ++k) {
+        float v = sum[half][k];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        const int key = r + 8 * k, t = T + half * kStep + key;
+        if (c == 0 && t < len) {
+          if (!((live[half] >> key) & 1u)) v = 0.f;  // a token on a page outside the pool receives nothing
+          w_row[t] = accumulate ? w_row[t] + v : v;
         }
       }
   }
@@ -650,6 +735,7 @@ __global__ void dense_init_kernel(unsigned char *ws, double base) {
   }
   if (idx < kMaxShared) {
     reinterpret_cast<int32_t *>(ws + kDenseCount)[idx] = 0;
+    if (idx == 0) reinterpret_cast<int32_t *>(ws + kDenseCount)[kMaxShared] = 0;
     reinterpret_cast<uint32_t *>(ws + kDenseRedo)[idx] = 0u;
   }
   if (idx == 0) {
@@ -666,12 +752,15 @@ int opt_in(K kernel, size_t bytes) {
   return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <bool SPLIT, bool PV>
-int run_rows(const DenseArgs &a, unsigned grid, float *lse, void *stream, const uint32_t *redo = nullptr,
-             int chunk_tiles = 0) {
-  int rc = opt_in(dense_rows_kernel<SPLIT, PV>, sizeof(RowsSmem));
+// Blocks of the rows kernel an SM holds.
+constexpr int blocks_per_sm(int nr) { return nr == 1 ? 2 : 1; }
+
+template <int NR, int MODE>
+int run_rows(const DenseArgs &a, int64_t items, int64_t grid, float *lse, uint32_t *redo, int chunk_tiles, void *stream) {
+  const int rc = opt_in(dense_rows_kernel<NR, MODE>, sizeof(RowsSmem<8 * NR>));
   if (rc) return rc;
-  dense_rows_kernel<SPLIT, PV><<<grid, kThreads, sizeof(RowsSmem), (cudaStream_t)stream>>>(a, lse, redo, chunk_tiles);
+  dense_rows_kernel<NR, MODE><<<(unsigned)grid, kThreads, sizeof(RowsSmem<8 * NR>), (cudaStream_t)stream>>>(
+      a, (int)items, lse, redo, chunk_tiles);
   return (int)cudaGetLastError();
 }
 
@@ -690,16 +779,18 @@ int launch_dense_init(void *ws, double base, void *stream) {
   return (int)cudaGetLastError();
 }
 
-// Blocks a tile's keys are shared among: enough for every SM, in waves as full as possible, as
-// long as a block keeps kMinKeys keys (below that the join costs more than the walk it saves).
-static int pick_split(int64_t items, int64_t max_keys, int sms) {
+// Blocks a tile's keys are shared among: enough for every place an SM has for a block, in waves
+// as full as possible, as long as a block keeps kMinKeys keys (below that the join costs more
+// than the walk it saves).
+static int pick_split(int64_t items, int64_t max_keys, int places, int rows) {
   constexpr int64_t kMinKeys = 256;
   if (items > kMaxShared) return 1;
-  const int64_t most = std::min<int64_t>({std::max<int64_t>(1, max_keys / kMinKeys), kRowsParts / items, 512});
+  const int64_t parts = (int64_t)(kDensePartBytes / (rows * kPartRow * sizeof(float)));
+  const int64_t most = std::min<int64_t>({std::max<int64_t>(1, max_keys / kMinKeys), parts / items, 512});
   int best = 1;
   double cost = 1e30;
   for (int64_t n = 1; n <= most; ++n) {
-    const int64_t waves = ceil_div(items * n, sms);
+    const int64_t waves = ceil_div(items * n, places);
     // a wave's time in keys walked, plus about 1000 keys' worth of a block's start and end
     const double c = (double)waves * ((double)max_keys / (double)n + 1000.0);
     if (c < cost * 0.995) {
@@ -711,24 +802,28 @@ static int pick_split(int64_t items, int64_t max_keys, int sms) {
   return best;
 }
 
-int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, void *stream) {
-  const int per = kRows >> a.group_shift;
+int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
+  // Tiles of 8 rows keep two blocks on an SM; more rows than that share a key's fetch and turn.
+  const int nr = ((int64_t)a.nq << a.group_shift) <= 8 ? 1 : 2;
+  const int per = (8 * nr) >> a.group_shift;
   a.tiles = (a.nq + per - 1) / per;
   const int64_t items = (int64_t)a.batch * a.hkv * a.tiles;
-  a.nsplit = pick_split(items, max_keys, dense_sm_count());
-  const unsigned grid = (unsigned)(items * a.nsplit);
-  if (lse) return run_rows<true, false>(a, grid, lse, stream);
-  return split ? run_rows<true, true>(a, grid, nullptr, stream) : run_rows<false, true>(a, grid, nullptr, stream);
+  a.nsplit = pick_split(items, max_keys, dense_sm_count() * blocks_per_sm(nr), 8 * nr);
+  const int64_t grid = items * a.nsplit;
+  if (lse)
+    return nr == 1 ? run_rows<1, 1>(a, items, grid, lse, nullptr, 0, stream)
+                   : run_rows<2, 1>(a, items, grid, lse, nullptr, 0, stream);
+  return nr == 1 ? run_rows<1, 0>(a, items, grid, nullptr, nullptr, 0, stream)
+                 : run_rows<2, 0>(a, items, grid, nullptr, nullptr, 0, stream);
 }
 
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream) {
-  const int per = kRows >> a.group_shift;
+  const int per = 16 >> a.group_shift;
   a.tiles = (a.nq + per - 1) / per;
   a.nsplit = 1;
+  const int64_t items = (int64_t)a.batch * a.hkv * a.tiles;
   uint32_t *redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(a.hdr) + kDenseRedo);
-  int rc = run_rows<true, true>(a, (unsigned)((int64_t)a.batch * a.hkv * a.tiles), nullptr, stream, redo, chunk_tiles);
-  if (rc) return rc;
-  return (int)cudaMemsetAsync(redo, 0, kMaxShared * sizeof(uint32_t), (cudaStream_t)stream);
+  return run_rows<2, 2>(a, items, std::min<int64_t>(items, dense_sm_count()), nullptr, redo, chunk_tiles, stream);
 }
 
 int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream) {

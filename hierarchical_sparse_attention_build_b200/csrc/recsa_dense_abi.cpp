@@ -105,8 +105,10 @@ recsa_status attend(DenseArgs a, void *out, int32_t out_is_fp32, size_t ws_bytes
   a.out = out;
   a.out_fp32 = out_is_fp32 ? 1 : 0;
   const int64_t rows = (int64_t)a.nq << a.group_shift;  // of a KV group
-  const int rc = !a.out_fp32 && rows >= kChunkRows ? launch_dense_chunk(a, max_keys(a), (int64_t)(ws_bytes - kDenseImages), stream)
-                                                   : launch_dense_rows(a, a.out_fp32 != 0, max_keys(a), nullptr, stream);
+  int rc = kNoRoom;
+  if (!a.out_fp32 && rows >= kChunkRows)
+    rc = launch_dense_chunk(a, max_keys(a), (int64_t)(ws_bytes - kDenseImages), stream);
+  if (rc == kNoRoom) rc = launch_dense_rows(a, max_keys(a), nullptr, stream);
   return rc != 0 ? cuda_fail(rc, "dense attend") : RECSA_OK;
 }
 
@@ -123,10 +125,13 @@ RECSA_API recsa_status recsa_dense_workspace_size(const recsa_params *params, in
   if (capacity > ((int64_t)1 << 30))
     return fail(RECSA_ERR_UNSUPPORTED, "capacity %lld > 2^30 tokens", (long long)capacity);
   if (!bytes_out) return fail(RECSA_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
-  // rotated images: the keys of every head, and as many rows of every query head
+  // rotated rows of the chunk kernel: all heads' keys and queries up to kMaxDenseImages, or else
+  // one head's keys (and an eighth of the room for its queries)
   const int64_t rows = std::min<int64_t>((capacity + 127) / 128 * 128 * batch, 1 << 20);
-  const int64_t images = rows * (params->num_kv_heads + 2 * (int64_t)params->num_q_heads) * kRowBytes + (1 << 20);
-  *bytes_out = kDenseImages + (size_t)std::min<int64_t>(images, kMaxDenseImages);
+  const int64_t all = rows * (params->num_kv_heads + 2 * (int64_t)params->num_q_heads) * kRowBytes * 9 / 8 + (1 << 20);
+  const int64_t head = (capacity + 127) / 128 * (128 * kRowBytes + 16) / 7 * 8 + (1 << 20);
+  const int64_t most = std::max<int64_t>(kMaxDenseImages, std::min<int64_t>(head, kMaxHeadImages));
+  *bytes_out = kDenseImages + (size_t)(std::min(all, most) + 255) / 256 * 256;
   return RECSA_OK;
 }
 
@@ -250,7 +255,7 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
   if (rows > kMaxDenseLse) return fail(RECSA_ERR_UNSUPPORTED, "%lld query rows > %lld", (long long)rows,
                                        (long long)kMaxDenseLse);
   float *lse = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kDenseLse);
-  int rc = launch_dense_rows(a, true, max_keys(a), lse, stream);
+  int rc = launch_dense_rows(a, max_keys(a), lse, stream);
   if (rc != 0) return cuda_fail(rc, "softmax sums");
   rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, stream);
   return rc != 0 ? cuda_fail(rc, "attention weights") : RECSA_OK;

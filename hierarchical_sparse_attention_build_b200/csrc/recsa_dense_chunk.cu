@@ -1,23 +1,31 @@
 // Dense attention of a chunk of queries on the 5th-generation tensor cores (bf16 outputs).
 //
-// A work item is 256 query rows (256 / G queries x the G heads of one KV group) of one
-// sequence, as two tiles of 128 rows; its keys come in tiles of 128.  One CTA per SM:
-//   warps 0-3, 4-7 : softmax of the two row tiles, a thread a row (scores and probabilities in
-//                    TMEM), the rescaling of the outputs and the epilogue;
-//   warps 8-11     : loaders: rotate the keys to their positions (registers -> swizzled shared
-//                    memory), gather the values with cp.async, rotate the queries;
-//   warp 12        : one thread issues the products: S = Q K^T (shared x shared) and
-//                    O += P V (TMEM x shared).
+// dense_images_kernel turns the keys and queries to their positions once and leaves them as the
+// tiles' shared-memory images, so that dense_chunk_kernel fetches a tile with one bulk copy
+// (turning the keys inside it, once a work item, took as many issue slots as the softmax: a
+// chunk of 4096 over 32768 tokens, 32 query heads, took 4.1 ms that way).
+//
+// dense_chunk_kernel: a work item is 256 query rows (256 / G queries x the G heads of one KV
+// group) of one sequence, as two tiles of 128 rows; its keys come in tiles of 128.  One CTA per SM:
+//   warps 0-3, 4-7 : softmax of the two row tiles, a thread a row with its 128 scores in
+//                    registers; the probabilities go over the scores in TMEM.  (Two threads a row
+//                    were slower: their exchange of maxima cost more than the shorter rows gave.)
+//   warps 8-11     : gather the values with cp.async (any page size) into swizzled tiles;
+//   warp 12        : one thread issues the products S = Q K^T (shared x shared) and O += P V
+//                    (TMEM x shared) of the two row tiles in turn;
+//   warp 13        : one thread copies the images.
 // While one row tile's softmax runs, the tensor cores do the other's O += P V and next S.
 //
-// Rounding: rotated queries and keys are rounded to fp16 (11 bits; half the steps of the
-// output's bf16 even after the sum over 128 terms), probabilities to bf16 (the values' type: one
-// product takes one type).  A rotated element beyond fp16's range, or an output that is not
-// finite (a hidden token's value may hold anything, and a zero weight times infinity is NaN),
-// marks the item: the rows kernel, which has neither limit, then computes it again.
+// Rounding: rotated queries and keys are rounded to fp16 (half a step is 2^-12 of an element:
+// an eighth of what bf16 would add to a score), probabilities to bf16 (the values' type: one
+// product takes one type; half a step, 2^-8 of a weight, as the output's own rounding).  A
+// rotated element beyond fp16's range, or an output that is not finite (a hidden token's value
+// may hold anything, and a zero weight times infinity is NaN), marks the item: the rows kernel,
+// which has neither limit, then computes it again.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -30,50 +38,51 @@ namespace {
 
 constexpr int kTile = 128;                  // rows of a row tile, keys of a key tile
 constexpr int kItemRows = 2 * kTile;
+constexpr int kStepKeys = 64;              // keys of a softmax step: half a key tile
 constexpr int kSoftWarps = 8;
 constexpr int kLoadThreads = 128;
+constexpr int kChunkThreads = 512;
 constexpr int kTileBytes = kTile * kRowBytes;  // 32 KB: [64-element half][row][128 bytes], 16-byte pieces XOR row % 8
 constexpr int kHalfBytes = kTileBytes / 2;
+constexpr int kQueryBytes = 2 * kTileBytes;
+constexpr int kQueryRows = 32;              // query rows a block of the images kernel turns
 constexpr int kRing = 2;                    // key and value tiles in shared memory
 constexpr int kMaxChunkBlocks = (int)(kDensePartBytes / (2 * kItemRows * kPartRow * sizeof(float)));
-constexpr int kImageTiles = 2;              // items a head from which images are made
-constexpr float kRescale = 8.f;             // a row's maximum may lag by 2^8 before its output is rescaled
+constexpr float kRescale = 64.f;            // a row's maximum may lag by 2^64 before its output is rescaled
 
 struct ChunkSmem {
   unsigned char q[2][kTileBytes];
   unsigned char k[kRing][kTileBytes];
   unsigned char v[kRing][kTileBytes];
-  uint32_t live[4][4][4];                   // a key tile's tokens that were loaded, by tile % 4: a part a loader warp
-  alignas(16) uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t join, joined, drain;
+  uint4 live[4];                            // a key tile's tokens that were loaded, by tile % 4
+  int gap[4];                               // whether some token of it before the sequence's end was not
+  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
+  uint64_t s_full[2][2], p_full[2][2];
+  uint64_t join, joined, drain[2];
   uint32_t tmem;
-  uint32_t stop;                            // a wait ran out: every role leaves
+  uint32_t stop;                            // a wait ran out: no role waits any more, all run to their ends
   int last;
-  int scan[16];
+  int scan[kChunkThreads / 32];
   int prefix[kMaxShared + 1];               // key tiles before each item, when items are shared
 };
-
 constexpr size_t kChunkSmem = sizeof(ChunkSmem) + 1024;  // the tiles begin on 1024 bytes
 
 struct ChunkArgs {
   DenseArgs d;
-  int bh0, heads;  // the launch's (sequence, KV head) pairs
-  int items;     // work items
-  int shared;    // 1: the key tiles of all items are dealt out evenly to the blocks
+  int bh0, heads;   // the launch's (sequence, KV head) pairs
+  int tile0, tiles; // and its items of each (of the d.tiles that the chunk has)
+  int items;
+  int shared;       // 1: the key tiles of all items are dealt out evenly to the blocks
+  int key_tiles, query_sets;
   uint32_t *redo;
-  // rotated rows as the tiles' shared-memory images (IMG): keys [heads][key_tiles], their loaded
-  // tokens, queries [items][1 or 2: for the window's tokens, for the sinks][2 row tiles]
+  // rotated rows: keys [heads][key_tiles] and their loaded tokens; queries [items][1 or 2: for the
+  // window's tokens, for the sinks][2 row tiles]
   unsigned char *key_images, *query_images;
   uint4 *live;
-  int key_tiles, query_sets;
 };
-__device__ __forceinline__ uint32_t &redo_mark(const ChunkArgs &a, int item) {
-  return a.redo[(a.bh0 * a.d.tiles + item) % kMaxShared];
-}
 
-__host__ __device__ constexpr uint32_t chunk_idesc(bool bf16, bool b_mn) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(kTile >> 3) << 17) |
+__host__ __device__ constexpr uint32_t chunk_idesc(int n, bool bf16, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kTile >> 4) << 24);
 }
 // Descriptor of a 128-byte-swizzled operand: rows of 128 bytes, 8 rows 1024 bytes apart.  K-major
@@ -82,6 +91,13 @@ __host__ __device__ constexpr uint32_t chunk_idesc(bool bf16, bool b_mn) {
 __device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo) {
   return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
+}
+// One thread of the warp, chosen so that the compiler knows only one runs on: descriptors then stay
+// in uniform registers (branching on the lane number instead doubled the cycles an MMA took).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -98,14 +114,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -120,11 +135,13 @@ struct Item {
   int hi1, n1;            // sinks: tokens, key tiles
   int lo2, hi2, first;    // the window's tokens; its first key tile
   int tiles;              // key tiles (at least one, which may hold nothing)
+  __device__ __forceinline__ bool sink(int j) const { return j < n1; }
+  __device__ __forceinline__ int token(int j) const { return (j < n1 ? j : first + j - n1) * kTile; }
 };
 __device__ __forceinline__ Item chunk_item(const ChunkArgs &a, int item) {
   const DenseArgs &d = a.d;
   Item it;
-  const int bh = a.bh0 + item / d.tiles, tile = d.tiles - 1 - item % d.tiles;  // the longest ranges first
+  const int bh = a.bh0 + item / a.tiles, tile = a.tile0 + a.tiles - 1 - item % a.tiles;  // the longest ranges first
   it.b = bh / d.hkv;
   it.h = bh % d.hkv;
   it.q0 = tile * (kItemRows >> d.group_shift);
@@ -139,6 +156,10 @@ __device__ __forceinline__ Item chunk_item(const ChunkArgs &a, int item) {
   it.first = it.lo2 / kTile;
   it.tiles = max(1, it.n1 + (it.hi2 > it.lo2 ? (it.hi2 + kTile - 1) / kTile - it.first : 0));
   return it;
+}
+// Where the rows kernel looks whether to compute a tile of the chunk again.
+__device__ __forceinline__ void mark_again(const ChunkArgs &a, int b, int h, int tile) {
+  a.redo[redo_slot(b * a.d.hkv + h, a.d.tiles, tile)] = 1u;
 }
 
 // The key tiles that some query of the chunk sees: those of the sinks, then the window's.
@@ -167,7 +188,7 @@ __device__ __forceinline__ Segments segments_begin(const ChunkArgs &a, const Chu
   Segments s;
   s.j0 = s.j1 = 0;
   s.at = s.end = s.begin = 0;
-  s.item = blockIdx.x;
+  s.item = (int)blockIdx.x - (int)gridDim.x;
   if (a.shared) {
     const int total = sm.prefix[a.items], blocks = sharing_blocks(total);
     if ((int)blockIdx.x >= blocks) return s;
@@ -179,8 +200,6 @@ __device__ __forceinline__ Segments segments_begin(const ChunkArgs &a, const Chu
       if (sm.prefix[mid] <= s.at) lo = mid; else hi = mid - 1;
     }
     s.item = lo - 1;
-  } else {
-    s.item -= gridDim.x;
   }
   return s;
 }
@@ -202,14 +221,23 @@ __device__ __forceinline__ bool segments_next(const ChunkArgs &a, const ChunkSme
   return true;
 }
 
-__device__ __forceinline__ bool wait_or_stop(ChunkSmem &sm, const ChunkArgs &a, uint64_t *bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kMbarPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*(volatile uint32_t *)&sm.stop) return false;
+// Waits for a barrier's phase, within a limit; after a wait ran out nobody waits any more (each
+// role's steps are counted, so all of them end) and the timeout is reported.
+// A poll without a suspend hint wakes sooner (a 4096-token chunk over 32768: 2.24 -> 2.16 ms).
+constexpr uint32_t kChunkPolls = 1u << 20;  // of a microsecond or so each
+__device__ __forceinline__ void wait(ChunkSmem &sm, const ChunkArgs &a, uint64_t *bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kChunkPolls; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return;
+    if (*(volatile uint32_t *)&sm.stop) return;
   }
   *(volatile uint32_t *)&sm.stop = 1u;
   atomicOr(&a.d.hdr->err, kErrTimeout);
-  return false;
 }
 
 // Rotation state of eight frequencies: cos and sin of a position, advanced by a fixed step.
@@ -263,21 +291,15 @@ __device__ __forceinline__ void put_row(unsigned char *tile, int row, int ch, co
   *reinterpret_cast<uint4 *>(p + kHalfBytes) = hi;
 }
 
-// The item's query rows, turned to their positions (sinks: their positions for the sinks).
-__device__ __forceinline__ void load_queries(const ChunkArgs &a, unsigned char *q, const Item &it, bool sink, int lt,
-                                             __half2 &most) {
+// Query rows row0 + 0 .. kQueryRows - 1 of an item into its image, turned to their positions
+// (sinks: to their positions for the sinks).
+__device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *q, const Item &it, bool sink, int row0,
+                                             int lt, __half2 &most) {
   const DenseArgs &d = a.d;
   const int ch = lt & 7, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
-  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
-  Turn t, step;
-  // rows lt / 8 + 16 i: for the window their positions advance by 16 / G a step
-  const bool even = !sink || !d.rank_sinks;
-  step.set(f, d.causal ? 16 >> gs : 0);
-  t.set(f, dense_position(d, it.len, it.q0 + ((lt >> 3) >> gs)));
-#pragma unroll 1
-  for (int i = 0; i < kItemRows / 16; ++i) {
-    const int row = (lt >> 3) + 16 * i, qi = row >> gs;
-    if (!even) t.set(f, sink_position(d, dense_position(d, it.len, it.q0 + qi)));
+#pragma unroll
+  for (int i = 0; i < kQueryRows / 16; ++i) {
+    const int row = row0 + (lt >> 3) + 16 * i, qi = row >> gs;
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
     if (qi < it.nq) {
       const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -285,10 +307,12 @@ __device__ __forceinline__ void load_queries(const ChunkArgs &a, unsigned char *
       lo = __ldg(src + ch);
       hi = __ldg(src + ch + 8);
     }
+    const int p = dense_position(d, it.len, it.q0 + qi);
+    Turn t;
+    t.set(ws_freq(d.hdr) + ch * 8, sink ? sink_position(d, p) : p);
     uint4 ol, oh;
     turn_row<true>(lo, hi, t, d.qscale, ol, oh, most);
     put_row(q + (row >> 7) * kTileBytes, row & 127, ch, ol, oh);
-    if (even) t.advance(step);
   }
 }
 
@@ -296,18 +320,20 @@ __device__ __forceinline__ bool beyond_half(__half2 most) {
   return __hgt(__hmax(__low2half(most), __high2half(most)), __float2half(65504.f));
 }
 
-// Rotated keys and queries of a launch as the chunk kernel's shared-memory images, so that it
-// fetches a tile with one bulk copy.  A block turns one key tile or one item's query rows.
-__global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a) {
+// Rotated keys (the first `keys` blocks: a key tile each) and queries (kQueryRows rows a block)
+// of a launch as the chunk kernel's images.
+__global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a, int keys) {
   const DenseArgs &d = a.d;
   if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the chunk kernel reports it
   const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3;
   __half2 most = __floats2half2_rn(0.f, 0.f);
-  const int keys = a.heads * a.key_tiles;
   if ((int)blockIdx.x >= keys) {
-    const int e = blockIdx.x - keys, item = e / a.query_sets;
-    load_queries(a, a.query_images + (int64_t)e * (2 * kTileBytes), chunk_item(a, item), e % a.query_sets == 1, lt, most);
-    if (beyond_half(most)) redo_mark(a, item) = 1u;
+    constexpr int kParts = kItemRows / kQueryRows;
+    const int e = blockIdx.x - keys, image = e / kParts, item = image / a.query_sets;
+    const Item it = chunk_item(a, item);
+    turn_queries(a, a.query_images + (int64_t)image * kQueryBytes, it, image % a.query_sets == 1, e % kParts * kQueryRows,
+                 lt, most);
+    if (beyond_half(most)) mark_again(a, it.b, it.h, it.q0 / (kItemRows >> d.group_shift));
     return;
   }
   const int hl = blockIdx.x / a.key_tiles, kt = blockIdx.x % a.key_tiles;
@@ -317,10 +343,6 @@ __global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a)
   if (kt >= hr.count) return;
   const int T = (kt < hr.n1 ? kt : hr.first + kt - hr.n1) * kTile;
   unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kTileBytes;
-  Turn t, step;
-  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
-  t.set(f, T + r0);
-  step.set(f, 16);
   uint32_t word[4] = {0u, 0u, 0u, 0u};
   uint4 xl[8], xh[8];
 #pragma unroll
@@ -339,6 +361,10 @@ __global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a)
       }
     }
   }
+  Turn t, step;
+  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
+  t.set(f, T + r0);
+  step.set(f, 16);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint4 ol, oh;
@@ -355,7 +381,7 @@ __global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a)
   __syncthreads();
   if (lt == 0) a.live[blockIdx.x] = make_uint4(words[0], words[1], words[2], words[3]);
   if (beyond_half(most))  // any of the head's items may read this tile
-    for (int tile_i = 0; tile_i < d.tiles; ++tile_i) redo_mark(a, hl * d.tiles + tile_i) = 1u;
+    for (int i = 0; i < d.tiles; ++i) mark_again(a, b, h, i);
 }
 
 // One bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
@@ -368,13 +394,45 @@ __device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// IMG: keys and queries come rotated, as images (dense_images_kernel); otherwise the loaders
-// rotate them.  Registers a thread: 16 warps launched with 128 give the softmax 192, the loaders
-// 72 and the last four warps 56 (65,536 in all); without images 13 warps launched with 128 give
-// 112, 152 and 128 (52,224 of 53,248).
-template <bool IMG>
-__global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkArgs a) {
-  constexpr int kChunkThreads = IMG ? 512 : 416;
+__device__ __forceinline__ float row_max(const uint32_t (&s)[2][32]) {
+  float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      x[g] = max3(x[g], __uint_as_float(s[g & 1][i + 2 * (g >> 1)]), __uint_as_float(s[g & 1][i + 2 * (g >> 1) + 1]));
+  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+}
+
+// A row's weights 2^(s - m) of half a key tile, rounded to bf16, over the scores in TMEM; returns
+// their sum and takes the scores' maximum into x.
+__device__ __forceinline__ float weigh(const uint32_t (&s)[2][32], float m, uint32_t ts, float &x) {
+  const float z = m == -INFINITY ? 0.f : m;
+  const F2 nz = f2(-z, -z);
+  F2 add = f2(0.f, 0.f);
+  float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float u = __uint_as_float(s[g][2 * i]), v = __uint_as_float(s[g][2 * i + 1]);
+      const float2 d = f2_get(f2_add(f2(u, v), nz));
+      const float2 e = make_float2(exp2_approx(d.x), exp2_approx(d.y));
+      add = f2_add(add, f2(e.x, e.y));
+      pk[i] = cvt_bf16x2(e.x, e.y);
+      if (i & 1)
+        x1 = max3(x1, u, v);
+      else
+        x0 = max3(x0, u, v);
+    }
+    tmem_st16(ts + g * 16, pk);
+  }
+  x = fmaxf(x0, x1);
+  return f2_get(add).x + f2_get(add).y;
+}
+
+__global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
   const DenseArgs &d = a.d;
@@ -385,19 +443,19 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
   }
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sm.k_full[i], IMG ? 1 : kLoadThreads);
+      mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.v_full[i], kLoadThreads);
-      mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.k_empty[i], 2);
+      mbar_init(&sm.v_empty[i], 2);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_full[t], 4);
-      mbar_init(&sm.o_full[t], 1);
+    for (int u = 0; u < 4; ++u) {
+      mbar_init(&sm.s_full[u & 1][u >> 1], 1);
+      mbar_init(&sm.p_full[u & 1][u >> 1], kSoftWarps / 2);
     }
     mbar_init(&sm.join, kSoftWarps);
     mbar_init(&sm.joined, 1);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.stop = 0;
     mbar_fence_init();
   }
@@ -435,147 +493,97 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
   Segments sg = segments_begin(a, sm);
   Item it;
 
+  // Registers a thread: 512 threads are launched with 128 (65,536); the softmax takes 176, the
+  // loaders 64 and the last four warps 96 of them (65,536).
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax and epilogue
-    if constexpr (IMG)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    const int t = warp >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int t = warp >> 2, trow = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t ts = tmem + lanes + t * kTile, to = tmem + lanes + 2 * kTile + t * kTile;
-    const int row = t * kTile + (warp & 3) * 32 + lane, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
-    uint32_t n_s = 0, n_o = 0, n_join = 0, n_tile = 0;  // phases of s_full, o_full and join, key tiles seen
-    bool ok = true;
-    while (ok && segments_next(a, sm, sg, it)) {
+    const int row = t * kTile + trow, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
+    uint32_t n = 0, n_s = 0, n_join = 0;  // key tiles seen; phases of s_full and join
+    while (segments_next(a, sm, sg, it)) {
       const bool in = (row >> gs) < it.nq;
-      const int p = in ? dense_position(d, it.len, it.q0 + (row >> gs)) : 0;
-      const int lo = window_first(d, p), hi = p, hi_sink = min(p, it.hi1);
+      const int p = in ? dense_position(d, it.len, it.q0 + (row >> gs)) : INT_MAX;  // rows past the chunk: no mask
+      const int lo = in ? window_first(d, p) : 0, hi_sink = min(p, it.hi1);
+      // every row of the warp sees tokens [lo_all, hi_all) of the window, [0, hi_sink_all) of the sinks
+      const int lo_all = __reduce_max_sync(0xffffffffu, lo), hi_all = __reduce_min_sync(0xffffffffu, p),
+                hi_sink_all = __reduce_min_sync(0xffffffffu, hi_sink);
       float m = -INFINITY, l = 0.f;
-      for (int j = sg.j0; j < sg.j1; ++j, ++n_tile) {
-        const bool sink = j < it.n1;
-        const int T = (sink ? j : it.first + j - it.n1) * kTile;
-        const int a0 = (sink ? 0 : lo) - T, a1 = (sink ? hi_sink : hi) - T;  // visible columns [a0, a1)
-        if (!wait_or_stop(sm, a, &sm.s_full[t], n_s & 1)) {
-          ok = false;
-          break;
-        }
-        ++n_s;
-        umma::fence_after_sync();
-        uint32_t live[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int w = 0; w < (IMG ? 1 : 4); ++w) {
-          const uint4 lv = *reinterpret_cast<const uint4 *>(sm.live[n_tile & 3][w]);
-          live[0] |= lv.x, live[1] |= lv.y, live[2] |= lv.z, live[3] |= lv.w;
-        }
-        const bool whole = a0 <= 0 && a1 >= kTile && (live[0] & live[1] & live[2] & live[3]) == 0xffffffffu;
-        const bool masked = __any_sync(0xffffffffu, !whole);
-        float x = -INFINITY;
-        [[maybe_unused]] uint32_t sr[IMG ? 4 : 1][32];  // the row's scores
-        if constexpr (IMG) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) umma::tmem_ld32(ts + g * 32, sr[g]);
+      for (int j = sg.j0; j < sg.j1; ++j, ++n, ++n_s) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int T = it.token(j) + h * kStepKeys;
+          const bool sink = it.sink(j);
+          wait(sm, a, &sm.s_full[t][h], n_s & 1);
+          umma::fence_after_sync();
+          const uint32_t tsh = ts + h * kStepKeys;
+          uint32_t s[2][32];
+          umma::tmem_ld32(tsh, s[0]);
+          umma::tmem_ld32(tsh + 32, s[1]);
+          const bool masked = sm.gap[n & 3] || T + kStepKeys > (sink ? hi_sink_all : hi_all) || (!sink && T < lo_all);
           umma::tmem_wait_ld();
           if (masked) {
+            const uint2 live = reinterpret_cast<const uint2 *>(&sm.live[n & 3])[h];
+            const int a0 = (sink ? 0 : lo) - T, a1 = (sink ? hi_sink : p) - T;  // visible columns [a0, a1)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int c = g * 32 + i;
-                if (c < a0 || c >= a1 || !((live[g] >> i) & 1u)) sr[g][i] = 0xff800000u;
-              }
+              for (int i = 0; i < 32; ++i)
+                if (g * 32 + i < a0 || g * 32 + i >= a1 || !(((g ? live.y : live.x) >> i) & 1u)) s[g][i] = 0xff800000u;
           }
-          float xs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) xs[g] = max3(xs[g], __uint_as_float(sr[g][i]), __uint_as_float(sr[g][i + 1]));
-          x = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3]));
-        } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t s[32];
-            umma::tmem_ld32(ts + g * 32, s);
-            umma::tmem_wait_ld();
-            if (masked) {
-              const uint32_t w = live[g];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int c = g * 32 + i;
-                if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) x = max3(x, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          }
-        }
-        const bool up = x > m + kRescale || (m == -INFINITY && x > m);
-        if (__any_sync(0xffffffffu, up)) {
-          const float f = up ? (m == -INFINITY ? 0.f : exp2_approx(m - x)) : 1.f;
-          if (up) {
-            m = x;
+          const bool first = j == sg.j0 && h == 0;
+          if (first) m = row_max(s);
+          // The weights are taken from the maximum so far, without waiting for this step's:
+          // weights, sums and outputs hold numbers up to 2^127 with the same relative precision.
+          // Only where a row's maximum has grown by more than 2^kRescale are they taken again
+          // (and its output rescaled).
+          float x, sum = weigh(s, m, tsh, x);
+          const bool up = x > m + kRescale || (m == -INFINITY && x > m);
+          if (__any_sync(0xffffffffu, up)) {
+            const float f = up ? (m == -INFINITY ? 0.f : exp2_approx(m - x)) : 1.f;
+            if (up) m = x;
             l *= f;
-          }
-          if (j > sg.j0) {
+            sum = weigh(s, m, tsh, x);
+            if (!first) {
+              // the last product into the output is complete once the other half's next scores are
+              wait(sm, a, &sm.s_full[t][h ^ 1], (n_s + h) & 1);
+              umma::fence_after_sync();
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-              uint32_t o[32];
-              umma::tmem_ld32(to + g * 32, o);
-              umma::tmem_wait_ld();
+              for (int g = 0; g < 8; ++g) {
+                uint32_t o[16];
+                tmem_ld16(to + g * 16, o);
+                umma::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(to + g * 32, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float z = m == -INFINITY ? 0.f : m;
-        const F2 nz = f2(-z, -z);
-        F2 sum = f2(0.f, 0.f);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t s[32], pk[16];
-          if constexpr (IMG) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = sr[g][i];
-          } else {
-            umma::tmem_ld32(ts + g * 32, s);
-            umma::tmem_wait_ld();
-            if (masked) {
-              const uint32_t w = live[g];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int c = g * 32 + i;
-                if (c < a0 || c >= a1 || !((w >> i) & 1u)) s[i] = 0xff800000u;
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(to + g * 16, o);
               }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x2 = f2_get(f2_add(f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), nz));
-            const float e0 = exp2_approx(x2.x), e1 = exp2_approx(x2.y);
-            sum = f2_add(sum, f2(e0, e1));
-            pk[i] = cvt_bf16x2(e0, e1);
-          }
-          tmem_st16(ts + g * 16, pk);  // over columns that were read
+          l += sum;
+          tmem_wait_st();
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[t][h]);
         }
-        l += f2_get(sum).x + f2_get(sum).y;
-        tmem_wait_st();
-        umma::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[t]);
       }
-      if (!ok || !wait_or_stop(sm, a, &sm.o_full[t], n_o & 1)) break;
-      ++n_o;
+      // s_full arrives once more after the segment's last products
+      wait(sm, a, &sm.s_full[t][0], n_s & 1);
+      wait(sm, a, &sm.s_full[t][1], n_s & 1);
+      ++n_s;
       umma::fence_after_sync();
-      // epilogue: the item's output, or this block's part of it
+      // epilogue: the item's output, or this block's part of it: [32 pieces of 16 bytes][row], then
+      // (maximum, sum) [row]
       const bool part = sg.j1 - sg.j0 < it.tiles;
-      const bool first_seg = sg.at - (sg.j1 - sg.j0) == sg.begin;
-      float *const pr = ws_part(d.hdr) + (((int64_t)blockIdx.x * 2 + (first_seg ? 0 : 1)) * kItemRows + row) * kPartRow;
+      auto part_of = [&](int c, bool first) {
+        return ws_part(d.hdr) + ((int64_t)c * 2 + (first ? 0 : 1)) * (kItemRows * kPartRow);
+      };
       const int64_t out_row = ((int64_t)it.b * d.nq + it.q0 + (row >> gs)) * hq + it.h * G + (row & (G - 1));
       uint4 *const po = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(d.out) + out_row * kD);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       bool odd = !(l < INFINITY);
+      float *const mypart = part_of(blockIdx.x, sg.at - (sg.j1 - sg.j0) == sg.begin);
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         uint32_t o[32];
@@ -584,25 +592,25 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(pr + 4 + g * 32 + i * 4) =
+            reinterpret_cast<uint4 *>(mypart)[(g * 8 + i) * kItemRows + row] =
                 make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else {
-          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float u = __uint_as_float(o[2 * i]) * inv, v = __uint_as_float(o[2 * i + 1]) * inv;
-            odd |= !(fabsf(u) < INFINITY) || !(fabsf(v) < INFINITY);
-            w[i] = cvt_bf16x2(u, v);
-          }
-          if (in) {
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) po[g * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int c = 0; c < 4; ++c) {
+              const float u = __uint_as_float(o[8 * i + 2 * c]) * inv, v = __uint_as_float(o[8 * i + 2 * c + 1]) * inv;
+              odd |= !(fabsf(u) < INFINITY) || !(fabsf(v) < INFINITY);
+              w[c] = cvt_bf16x2(u, v);
+            }
+            if (in) po[g * 4 + i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
       umma::fence_before_sync();
       if (part) {
-        *reinterpret_cast<float2 *>(pr) = make_float2(m, l);
+        reinterpret_cast<float2 *>(mypart + kItemRows * kD)[row] = make_float2(m, l);
         odd = false;
         // the item's key tiles are spread over blocks c0 .. c1: the last to arrive joins them in order
         const int total = sm.prefix[a.items], blocks = sharing_blocks(total);
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
         __threadfence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.join);
-        if (!wait_or_stop(sm, a, &sm.join, n_join & 1)) break;
+        wait(sm, a, &sm.join, n_join & 1);
         if (tid == 0) {
           const int done = atomicAdd(ws_count(d.hdr) + sg.item, 1);
           sm.last = done == c1 - c0;
@@ -625,204 +633,116 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
           __threadfence();
           mbar_arrive(&sm.joined);
         }
-        if (!wait_or_stop(sm, a, &sm.joined, n_join & 1)) break;
+        wait(sm, a, &sm.joined, n_join & 1);
         ++n_join;
         __threadfence();
         if (sm.last) {
-          auto from = [&](int c) {
-            // the item is in block c's first segment if the block begins inside it
-            return ws_part(d.hdr) +
-                   (((int64_t)c * 2 + (dealt(total, blocks, c) >= w0 ? 0 : 1)) * kItemRows + row) * kPartRow;
-          };
+          // the item is in block c's first segment if the block begins inside it
+          auto from = [&](int c) { return part_of(c, dealt(total, blocks, c) >= w0); };
+          auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(from(c) + kItemRows * kD) + row); };
           float mm = -INFINITY, ll = 0.f;
-          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(from(c)));
+          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, stats(c).x);
           for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(from(c)));
+            const float2 ml = stats(c);
             if (ml.x != -INFINITY) ll += ml.y * exp2_approx(ml.x - mm);
           }
           const float iv = ll == 0.f ? 0.f : 1.f / ll;
           odd = !(ll < INFINITY);
 #pragma unroll 1
-          for (int g = 0; g < 16; ++g) {
-            float acc[8] = {};
+          for (int g = 0; g < 4; ++g) {
+            float acc[32] = {};
             for (int c = c0; c <= c1; ++c) {
-              const float *q = from(c);
-              const float mc = __ldcg(q);
+              const float mc = stats(c).x;
+              const float4 *src = reinterpret_cast<const float4 *>(from(c)) + g * 8 * kItemRows + row;
+              float4 u[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) u[i] = __ldcg(src + i * kItemRows);
               if (mc == -INFINITY) continue;
               const float f = exp2_approx(mc - mm) * iv;
-              const float4 u = __ldcg(reinterpret_cast<const float4 *>(q + 4 + g * 8));
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + 8 + g * 8));
-              acc[0] += f * u.x, acc[1] += f * u.y, acc[2] += f * u.z, acc[3] += f * u.w;
-              acc[4] += f * v.x, acc[5] += f * v.y, acc[6] += f * v.z, acc[7] += f * v.w;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[4 * i] += f * u[i].x, acc[4 * i + 1] += f * u[i].y;
+                acc[4 * i + 2] += f * u[i].z, acc[4 * i + 3] += f * u[i].w;
+              }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) odd |= !(fabsf(acc[i]) < INFINITY);
-            if (in)
-              po[g] = make_uint4(cvt_bf16x2(acc[0], acc[1]), cvt_bf16x2(acc[2], acc[3]), cvt_bf16x2(acc[4], acc[5]),
-                                 cvt_bf16x2(acc[6], acc[7]));
+            for (int i = 0; i < 32; ++i) odd |= !(fabsf(acc[i]) < INFINITY);
+            if (in) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                po[g * 4 + i] = make_uint4(cvt_bf16x2(acc[8 * i], acc[8 * i + 1]), cvt_bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
+                                           cvt_bf16x2(acc[8 * i + 4], acc[8 * i + 5]),
+                                           cvt_bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
+            }
           }
         }
       }
-      if (odd && in) redo_mark(a, sg.item) = 1u;
+      if (odd && in) mark_again(a, it.b, it.h, it.q0 / (kItemRows >> gs));
     }
   } else if (warp < 12) {
-    // ------------------------------------------------------------------ loaders
-    if constexpr (IMG)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    const int lt = tid - kSoftWarps * 32, ch = lt & 7;
-    const uint64_t *f = ws_freq(d.hdr) + ch * 8;
-    const int r0 = lt >> 3;  // this thread's rows: r0 + 16 i
-    [[maybe_unused]] Turn step, t;
-    if constexpr (!IMG) step.set(f, 16);
+    // ------------------------------------------------------------------ values
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    const int lt = tid - kSoftWarps * 32, ch = lt & 7, r0 = lt >> 3;  // rows r0 + 16 i
+    const uint32_t sv = smem_u32(sm.v[0]) + r0 * 128 + ((ch ^ (r0 & 7)) << 4);
     uint32_t n = 0;  // key tiles loaded
-    bool ok = true;
-    while (ok && segments_next(a, sm, sg, it)) {
-      __half2 most = __floats2half2_rn(0.f, 0.f);
-      // Rows of key tile j in the caches (fewer than 2^32 rows fit a GPU); bit i of the result:
-      // this thread's row i is a token of the range on a page of the pool.
-      uint32_t rows[8], here;
+    while (segments_next(a, sm, sg, it)) {
+      uint32_t rows[8], here = 0;  // rows in the cache (fewer than 2^32 fit a GPU); bit i: row i is a token to load
       auto place = [&](int j) {
-        const bool sink = j < it.n1;
-        const int T = (sink ? j : it.first + j - it.n1) * kTile;
-        const int lo = sink ? 0 : it.lo2, hi = sink ? it.hi1 : it.hi2;
+        const int T = it.token(j), lo = it.sink(j) ? 0 : it.lo2, hi = it.sink(j) ? it.hi1 : it.hi2;
         here = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int tok = T + r0 + 16 * i;
-          rows[i] = 0;
-          if (tok >= lo && tok < hi) {
-            const int64_t r = cache_row(d, it.b, it.h, tok);
-            if (r >= 0) {
-              rows[i] = (uint32_t)r;
-              here |= 1u << i;
-            } else if (!IMG) {
-              atomicOr(&d.hdr->err, kErrIndex);
-            }
-          }
-        }
-      };
-      [[maybe_unused]] uint4 xl[2][4], xh[2][4];  // raw keys of half a tile, the next half in flight while one is turned
-      auto fetch = [&](int hf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool on = (here >> (hf * 4 + i)) & 1u;
-          const uint4 *src = reinterpret_cast<const uint4 *>(d.k + (int64_t)rows[hf * 4 + i] * kD);
-          xl[hf][i] = on ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
-          xh[hf][i] = on ? __ldg(src + ch + 8) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto turn = [&](int hf, int s) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 ol, oh;
-          turn_row<false>(xl[hf][i], xh[hf][i], t, 1.f, ol, oh, most);
-          put_row(sm.k[s], r0 + 16 * (hf * 4 + i), ch, ol, oh);
-          t.advance(step);
+          const int64_t r = tok >= lo && tok < hi ? cache_row(d, it.b, it.h, tok) : -1;
+          rows[i] = r >= 0 ? (uint32_t)r : 0u;
+          here |= r >= 0 ? 1u << i : 0u;
         }
       };
       place(sg.j0);
-      if constexpr (!IMG) fetch(0);
       for (int j = sg.j0; j < sg.j1; ++j, ++n) {
-        const bool sink = j < it.n1;
         const int s = n % kRing;
-        const uint32_t round = n / kRing;
-        if (!IMG && (j == sg.j0 || (j == it.n1 && j > 0))) {
-          // the queries of a new segment, or of the window after the sinks: the products that
-          // read the last ones are done once the previous key tile is free
-          if (n > 0 && !wait_or_stop(sm, a, &sm.k_empty[(n - 1) % kRing], ((n - 1) / kRing) & 1)) {
-            ok = false;
-            break;
-          }
-          load_queries(a, sm.q[0], it, sink, lt, most);
-        }
-        // The rotation goes on from tile to tile (16 positions a row, 128 a tile) and starts anew
-        // every 16 tiles: 128 steps of fp32 rounding are below 2^-16, fp16 rounds at 2^-11.
-        if (!IMG && (j == sg.j0 || j == it.n1 || ((j - sg.j0) & 15) == 0))
-          t.set(f, (sink ? j : it.first + j - it.n1) * kTile + r0);
-        if (round > 0 && !wait_or_stop(sm, a, &sm.v_empty[s], (round - 1) & 1)) {
-          ok = false;
-          break;
-        }
+        if (n >= kRing) wait(sm, a, &sm.v_empty[s], (n / kRing - 1) & 1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t dst = smem_u32(sm.v[s]) + (r0 + 16 * i) * 128 + ((ch ^ (r0 & 7)) << 4);
+          const uint32_t dst = sv + s * kTileBytes + i * 16 * 128;
           const bool on = (here >> i) & 1u;
           const uint16_t *src = d.v + (int64_t)rows[i] * kD + ch * 8;
           cp_async16(dst, src, on);
           cp_async16(dst + kHalfBytes, src + kHalf, on);
         }
         cp_async_commit();
-        if constexpr (IMG) {
-          if (j + 1 < sg.j1) place(j + 1);
-          cp_async_wait<0>();
-          umma::fence_async_smem();
-          mbar_arrive(&sm.v_full[s]);
-          continue;
-        }
-        fetch(1);
-        if (round > 0 && !wait_or_stop(sm, a, &sm.k_empty[s], (round - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        {  // live tokens, each warp its rows: word w of the tile is tokens 32 w .. 32 w + 31
-          uint32_t word[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) word[i >> 1] |= ((here >> i) & 1u) << (r0 + 16 * (i & 1));
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            word[w] |= __shfl_xor_sync(0xffffffffu, word[w], 8);
-            word[w] |= __shfl_xor_sync(0xffffffffu, word[w], 16);
-          }
-          if (lane == 0)
-            *reinterpret_cast<uint4 *>(sm.live[n & 3][warp - kSoftWarps]) = make_uint4(word[0], word[1], word[2], word[3]);
-        }
-        turn(0, s);
-        if (j + 1 < sg.j1) {
-          place(j + 1);
-          fetch(0);
-        }
-        turn(1, s);
-        umma::fence_async_smem();
-        mbar_arrive(&sm.k_full[s]);
+        if (j + 1 < sg.j1) place(j + 1);
         cp_async_wait<0>();
         umma::fence_async_smem();
         mbar_arrive(&sm.v_full[s]);
       }
-      if (!IMG && beyond_half(most)) redo_mark(a, sg.item) = 1u;
     }
-    cp_async_wait<0>();
   } else {
-    if constexpr (IMG) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (IMG && warp == 13 && lane == 0) {
+    if (warp == 13 && elect_one()) {
       // ---------------------------------------------------------------- images
       uint32_t n = 0;
-      bool ok = true;
-      while (ok && segments_next(a, sm, sg, it)) {
+      while (segments_next(a, sm, sg, it)) {
         const HeadRange hr = head_range(d, it.len);
         const int hl = it.b * d.hkv + it.h - a.bh0;
         for (int j = sg.j0; j < sg.j1; ++j, ++n) {
-          const bool sink = j < it.n1;
+          const bool sink = it.sink(j);
           const int s = n % kRing;
           const int kt = min(sink ? j : hr.n1 + it.first + j - it.n1 - hr.first, a.key_tiles - 1);
           const int64_t image = (int64_t)hl * a.key_tiles + kt;
           const bool queries = j == sg.j0 || (j == it.n1 && j > 0);
           // new queries: the products that read the last ones are done once the previous tile is free
-          if (queries && n > 0 && !wait_or_stop(sm, a, &sm.k_empty[(n - 1) % kRing], ((n - 1) / kRing) & 1)) {
-            ok = false;
-            break;
-          }
-          if (n >= kRing && !wait_or_stop(sm, a, &sm.k_empty[s], (n / kRing - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          *reinterpret_cast<uint4 *>(sm.live[n & 3][0]) = __ldg(a.live + image);
-          mbar_expect(&sm.k_full[s], kTileBytes + (queries ? 2 * kTileBytes : 0));
+          if (queries && n > 0) wait(sm, a, &sm.k_empty[(n - 1) % kRing], ((n - 1) / kRing) & 1);
+          if (n >= kRing) wait(sm, a, &sm.k_empty[s], (n / kRing - 1) & 1);
+          const uint4 live = __ldg(a.live + image);
+          const int left = it.len - it.token(j);  // tokens of the tile
+          const int have = __popc(live.x) + __popc(live.y) + __popc(live.z) + __popc(live.w);
+          sm.live[n & 3] = live;
+          sm.gap[n & 3] = have < min(left, kTile);
+          mbar_expect(&sm.k_full[s], kTileBytes + (queries ? kQueryBytes : 0));
           if (queries)
             bulk_load(smem_u32(sm.q[0]),
-                      a.query_images + ((int64_t)sg.item * a.query_sets + (sink ? 1 : 0)) * (2 * kTileBytes),
-                      2 * kTileBytes, &sm.k_full[s]);
+                      a.query_images + ((int64_t)sg.item * a.query_sets + (sink && a.query_sets == 2 ? 1 : 0)) * kQueryBytes,
+                      kQueryBytes, &sm.k_full[s]);
           bulk_load(smem_u32(sm.k[s]), a.key_images + image * kTileBytes, kTileBytes, &sm.k_full[s]);
         }
       }
@@ -830,88 +750,61 @@ __global__ void __launch_bounds__(IMG ? 512 : 416, 1) dense_chunk_kernel(ChunkAr
       if (n > 0) mbar_wait(&sm.k_full[(n - 1) % kRing], ((n - 1) / kRing) & 1);
       if (n > 1) mbar_wait(&sm.k_full[(n - 2) % kRing], ((n - 2) / kRing) & 1);
     }
-  }
-  if (warp == 12 && lane == 0) {
-    // ------------------------------------------------------------------ products
-    uint32_t n = 0;         // key tiles
-    uint32_t n_p = 0;       // phases of p_full
-    bool ok = true;
-    auto scores = [&](int t, int s) {
-      const uint32_t q = smem_u32(sm.q[t]), k = smem_u32(sm.k[s]);
+    if ((warp == 12 || warp == 14) && elect_one()) {
+      // ---------------------------------------------------------------- products
+      const int t = warp == 14;
+      const uint32_t ts = tmem + t * kTile, to = tmem + 2 * kTile + t * kTile;
+      const uint64_t dq = swizzled_desc(smem_u32(sm.q[t]), 16), dk = swizzled_desc(smem_u32(sm.k[0]), 16),
+                     dv = swizzled_desc(smem_u32(sm.v[0]), kHalfBytes);
+      uint32_t n = 0;  // key tiles
+      auto scores = [&](int h, uint32_t i) {
+        const uint64_t k = dk + (i % kRing) * (kTileBytes >> 4) + h * ((kStepKeys * 128) >> 4);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
-        umma::mma(tmem + t * kTile, swizzled_desc(q + off, 16), swizzled_desc(k + off, 16), chunk_idesc(false, false),
-                  ks > 0);
-      }
-      umma::commit(&sm.s_full[t]);
-    };
-    while (ok && segments_next(a, sm, sg, it)) {
-      const int count = sg.j1 - sg.j0;
-      if (!wait_or_stop(sm, a, &sm.k_full[n % kRing], (n / kRing) & 1)) break;
-      umma::fence_after_sync();
-      scores(0, n % kRing);
-      scores(1, n % kRing);
-      umma::commit(&sm.k_empty[n % kRing]);
-      for (int j = 0; j < count; ++j, ++n, ++n_p) {
-        const int s = n % kRing, s1 = (n + 1) % kRing;
-        if (!wait_or_stop(sm, a, &sm.v_full[s], (n / kRing) & 1)) {
-          ok = false;
-          break;
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+          umma::mma(ts + h * kStepKeys, dq + off, k + off, chunk_idesc(kStepKeys, false, false), ks > 0);
         }
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          if (!wait_or_stop(sm, a, &sm.p_full[t], n_p & 1)) {
-            ok = false;
-            break;
-          }
-          umma::fence_after_sync();
-          const uint32_t v = smem_u32(sm.v[s]);
+      };
+      while (segments_next(a, sm, sg, it)) {
+        const int count = sg.j1 - sg.j0;
+        wait(sm, a, &sm.k_full[n % kRing], (n / kRing) & 1);
+        umma::fence_after_sync();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_tmem_a(tmem + 2 * kTile + t * kTile, tmem + t * kTile + ks * 8, swizzled_desc(v + ks * 2048, kHalfBytes),
-                       chunk_idesc(true, true), j > 0 || ks > 0);
-          if (t == 1) umma::commit(&sm.v_empty[s]);
-          if (j + 1 < count) {
-            if (t == 0) {
-              if (!wait_or_stop(sm, a, &sm.k_full[s1], ((n + 1) / kRing) & 1)) {
-                ok = false;
-                break;
-              }
-              umma::fence_after_sync();
-            }
-            scores(t, s1);
-            if (t == 1) umma::commit(&sm.k_empty[s1]);
-          } else {
-            umma::commit(&sm.o_full[t]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          scores(h, n);
+          umma::commit(&sm.s_full[t][h]);
         }
-        if (!ok) break;
+        umma::commit(&sm.k_empty[n % kRing]);
+        for (int j = 0; j < count; ++j, ++n) {
+          const uint32_t s = n % kRing, s1 = (n + 1) % kRing;
+          const bool more = j + 1 < count;
+          wait(sm, a, &sm.v_full[s], (n / kRing) & 1);
+          if (more) wait(sm, a, &sm.k_full[s1], ((n + 1) / kRing) & 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wait(sm, a, &sm.p_full[t][h], n & 1);
+            umma::fence_after_sync();
+            const uint64_t v = dv + s * (kTileBytes >> 4) + h * ((kStepKeys * 128) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_tmem_a(to, ts + h * kStepKeys + ks * 8, v + ks * (2048 >> 4), chunk_idesc(kTile, true, true),
+                         j + h + ks > 0);
+            if (more) scores(h, n + 1);
+            umma::commit(&sm.s_full[t][h]);
+          }
+          umma::commit(&sm.v_empty[s]);
+          if (more) umma::commit(&sm.k_empty[s1]);
+        }
       }
+      umma::commit(&sm.drain[t]);  // nothing may be in flight when the tensor memory is freed
+      if (!mbar_wait(&sm.drain[t], 0)) atomicOr(&d.hdr->err, kErrTimeout);
     }
-    umma::commit(&sm.drain);  // nothing may be in flight when the tensor memory is freed
-    if (!mbar_wait(&sm.drain, 0)) atomicOr(&d.hdr->err, kErrTimeout);
   }
   __syncwarp();
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   if (warp == 12) umma::tmem_dealloc(tmem, 512);
-}
-
-}  // namespace
-
-namespace {
-
-template <bool IMG>
-int run_chunk(const ChunkArgs &a, int64_t tiles, void *stream) {
-  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
-  cudaError_t e = cudaFuncSetAttribute(dense_chunk_kernel<IMG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kChunkSmem);
-  if (e != cudaSuccess) return (int)e;
-  const int64_t work = a.shared ? a.items * tiles : a.items;
-  dense_chunk_kernel<IMG><<<(unsigned)std::min<int64_t>(work, sms), IMG ? 512 : 416, kChunkSmem, (cudaStream_t)stream>>>(a);
-  return (int)cudaGetLastError();
 }
 
 // The most key tiles a head's queries see.
@@ -928,40 +821,45 @@ int launch_dense_chunk(const DenseArgs &d, int64_t max_keys, int64_t image_bytes
   ChunkArgs a = {};
   a.d = d;
   const int per = kItemRows >> d.group_shift;
-  a.d.tiles = (d.nq + per - 1) / per;
-  const int64_t heads = (int64_t)d.batch * d.hkv;
+  const int64_t chunk_tiles = ceil_div(d.nq, per), heads = (int64_t)d.batch * d.hkv;
+  a.d.tiles = (int)chunk_tiles;
   a.redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(d.hdr) + kDenseRedo);
-  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
-  const int64_t tiles = ceil_div(max_keys, kTile) + 1;
-  // Rotated images pay once two items share a key tile; as many heads a launch as they fit.
   a.key_tiles = (int)most_key_tiles(d);
   a.query_sets = d.window && d.sinks && d.rank_sinks ? 2 : 1;
-  const int64_t head_bytes = a.key_tiles * (int64_t)(kTileBytes + sizeof(uint4)) +
-                             (int64_t)a.d.tiles * a.query_sets * 2 * kTileBytes;
-  const int64_t fit = image_bytes / head_bytes;
-  const bool images = a.d.tiles >= kImageTiles && fit >= 1;
-  const int64_t step = images ? std::min(heads, fit) : heads;
+  const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
+  cudaError_t e = cudaFuncSetAttribute(dense_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkSmem);
+  if (e != cudaSuccess) return (int)e;
+  // As many heads and items a launch as the images' room holds: an eighth of it for the queries
+  // of one head, at least one item.
+  const int64_t key_bytes = a.key_tiles * (int64_t)(kTileBytes + sizeof(uint4)), item_bytes = a.query_sets * (int64_t)kQueryBytes;
+  const int64_t head_tiles = std::min(chunk_tiles, std::max<int64_t>(1, image_bytes / 8 / item_bytes));
+  const int64_t fit = image_bytes / (key_bytes + head_tiles * item_bytes);
+  if (fit < 1) return kNoRoom;
+  const int64_t step = std::min(heads, fit), tiles = ceil_div(max_keys, kTile) + 1;
   for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
     a.bh0 = (int)bh0;
     a.heads = (int)std::min(step, heads - bh0);
-    a.items = a.heads * a.d.tiles;
-    // Dealing the key tiles out evenly costs a part's write and join (about four key tiles'
-    // time) and saves the last wave's idle blocks.
-    const int64_t plain = ceil_div(a.items, sms) * tiles, dealt = ceil_div(a.items * tiles, sms) + 4;
-    a.shared = a.items <= kMaxShared && dealt < plain ? 1 : 0;
-    int rc;
-    if (images) {
-      a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
-      a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kTileBytes;
-      a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.items * a.query_sets * 2 * kTileBytes);
-      dense_images_kernel<<<(unsigned)(a.heads * a.key_tiles + a.items * a.query_sets), kLoadThreads, 0,
-                            (cudaStream_t)stream>>>(a);
-      rc = (int)cudaGetLastError();
-      if (rc == 0) rc = run_chunk<true>(a, tiles, stream);
-    } else {
-      rc = run_chunk<false>(a, tiles, stream);
+    a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
+    a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kTileBytes;
+    a.live = reinterpret_cast<uint4 *>(a.query_images + a.heads * head_tiles * item_bytes);
+    for (int64_t tile0 = 0; tile0 < chunk_tiles; tile0 += head_tiles) {
+      a.tile0 = (int)tile0;
+      a.tiles = (int)std::min(head_tiles, chunk_tiles - tile0);
+      a.items = a.heads * a.tiles;
+      // Dealing the key tiles out evenly costs a part's write and join (about four key tiles'
+      // time) and saves the last wave's idle blocks.
+      const int64_t plain = ceil_div(a.items, sms) * tiles, dealt = ceil_div(a.items * tiles, sms) + 4;
+      a.shared = a.items <= kMaxShared && dealt < plain ? 1 : 0;
+      const int keys = tile0 == 0 ? a.heads * a.key_tiles : 0;
+      dense_images_kernel<<<(unsigned)(keys + (int64_t)a.items * a.query_sets * (kItemRows / kQueryRows)), kLoadThreads, 0,
+                            (cudaStream_t)stream>>>(a, keys);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return (int)e;
+      const int64_t work = a.shared ? a.items * tiles : a.items;
+      dense_chunk_kernel<<<(unsigned)std::min<int64_t>(work, sms), kChunkThreads, kChunkSmem, (cudaStream_t)stream>>>(a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return (int)e;
     }
-    if (rc) return rc;
   }
   return launch_dense_redo(d, a.d.tiles, stream);
 }

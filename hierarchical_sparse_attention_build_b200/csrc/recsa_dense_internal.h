@@ -16,13 +16,14 @@ constexpr int kMaxShared = 4096;               // work items whose key range may
 constexpr size_t kDenseFreq = kWsHeader;                                   // uint64[64] turns
 constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float2[64][64] (cos, sin)
 constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
-constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t);  // marks of items to compute again
+constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t) + 256;  // marks of items to compute again
 constexpr size_t kDensePart = kDenseRedo + kMaxShared * sizeof(uint32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
 constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call
 constexpr size_t kDenseImages = kDenseLse + kMaxDenseLse * sizeof(float);   // rotated rows of a chunk's keys and queries
-constexpr size_t kMaxDenseImages = (size_t)320 << 20;
+constexpr size_t kMaxDenseImages = (size_t)320 << 20;   // for many heads together
+constexpr size_t kMaxHeadImages = (size_t)1280 << 20;   // for one long head
 constexpr int kPartRow = kD + 4;  // floats of a row's partial result: maximum, sum, 2 unused, 128 sums
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -45,16 +46,23 @@ struct DenseArgs {
   WsHeader *hdr;
 };
 
+// Mark of tile `tile` (256 query rows) of a (sequence, KV head) in the workspace's list; two tiles
+// that share a mark are both computed again.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int redo_slot(int bh, int tiles, int tile) { return (int)(((int64_t)bh * tiles + tile) % kMaxShared); }
+
 int dense_sm_count();  // of the current device
 int launch_dense_init(void *ws, double base, void *stream);
-int launch_dense_rows(DenseArgs a, bool split, int64_t max_keys, float *lse, void *stream);
-// The chunk kernel (bf16 output), then the rows kernel for the items it marked.
+int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
+// The chunk kernel (bf16 output), then the rows kernel for the items it marked; kNoRoom, with
+// nothing launched, where a head's rotated keys do not fit image_bytes of the workspace.
+constexpr int kNoRoom = -1000;
 int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, int64_t image_bytes, void *stream);
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
 int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
                          int count, int64_t limit, void *stream);
-// Partial results a launch may leave in the workspace.
-constexpr int64_t kRowsParts = (int64_t)(kDensePartBytes / (16 * kPartRow * sizeof(float)));
 
 }  // namespace recsa
