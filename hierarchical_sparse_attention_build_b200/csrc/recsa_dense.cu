@@ -32,34 +32,71 @@ struct RowsSmem {
 };
 
 // One step's rows: 16 keys from token T, those outside [lo, hi) or on a page outside the pool as
-// zeros.  A lane places the row of key lane % 16; `live` are the keys that are there.
+// zeros; `live` are the keys that are there.  T is a multiple of 16, so a contiguous cache and
+// pages of 16 tokens or more hold a step in consecutive rows: its first row is enough then;
+// smaller pages place a row a lane (key lane % 16).
 struct Step {
-  int64_t row;
+  uint32_t row;   // fewer than 2^32 rows fit a GPU
   uint32_t live;
 };
 __device__ __forceinline__ Step place_step(const DenseArgs &a, int b, int h, int T, int lo, int hi, int lane) {
-  const int t = T + (lane & 15);
   Step s;
+  if (!a.pages || a.page_shift >= 4) {
+    const int64_t r = cache_row(a, b, h, T);
+    s.live = 0xffffu;
+    if (T < lo) s.live &= lo - T >= kStep ? 0u : 0xffffu << (lo - T);
+    if (T + kStep > hi) s.live &= hi <= T ? 0u : 0xffffu >> (T + kStep - hi);
+    if (r < 0 && s.live) {
+      if (lane == 0) atomicOr(&a.hdr->err, kErrIndex);
+      s.live = 0;
+    }
+    s.row = r < 0 ? 0u : (uint32_t)r;
+    return s;
+  }
+  const int t = T + (lane & 15);
   bool on = t >= lo && t < hi;
   s.row = 0;
   if (on) {
-    s.row = cache_row(a, b, h, t);
-    if (s.row < 0) {
-      s.row = 0;
+    const int64_t r = cache_row(a, b, h, t);
+    if (r < 0) {
       on = false;
       atomicOr(&a.hdr->err, kErrIndex);
+    } else {
+      s.row = (uint32_t)r;
     }
   }
   s.live = __ballot_sync(0xffffffffu, on) & 0xffffu;
   return s;
 }
-__device__ __forceinline__ void load_step(const uint16_t *cache, const Step &s, uint32_t dst, int lane) {
-  const int c = lane & 15;
+// A lane copies 16 bytes of keys 2 i + lane / 16; `swz` is where those of key lane / 16 go.
+__device__ __forceinline__ void load_step(const DenseArgs &a, const uint16_t *cache, const Step &s, uint32_t dst,
+                                          int lane) {
+  const int c = lane & 15, k0 = lane >> 4;
+  const uint32_t swz = dst + k0 * kRowBytes;
+  const uint32_t col = (uint32_t)((c ^ k0) << 4);  // piece c of key k goes to place c ^ (k % 8)
+  if (!a.pages || a.page_shift >= 4) {
+    const char *src = reinterpret_cast<const char *>(cache) + ((int64_t)s.row + k0) * kRowBytes + c * 16;
+    if (s.live == 0xffffu) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int key = 2 * i + (lane >> 4);
-    const int64_t r = __shfl_sync(0xffffffffu, s.row, key);
-    cp_async16(dst + key * kRowBytes + ((c ^ (key & 7)) << 4), cache + r * kD + c * 8, (s.live >> key) & 1u);
+      for (int i = 0; i < 8; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(swz + i * 2 * kRowBytes + (col ^ ((2 * i & 6) << 4))),
+                     "l"(src + i * 2 * kRowBytes)
+                     : "memory");
+    } else {  // rows outside the range are not touched: their source is the first row of the cache
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = (s.live >> (2 * i + k0)) & 1u;
+        cp_async16(swz + i * 2 * kRowBytes + (col ^ ((2 * i & 6) << 4)),
+                   on ? src + i * 2 * kRowBytes : reinterpret_cast<const char *>(cache), on);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t r = __shfl_sync(0xffffffffu, s.row, 2 * i + k0);
+      cp_async16(swz + i * 2 * kRowBytes + (col ^ ((2 * i & 6) << 4)), cache + (int64_t)r * kD + c * 8,
+                 (s.live >> (2 * i + k0)) & 1u);
+    }
   }
   cp_async_commit();
 }
@@ -105,10 +142,6 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
   const unsigned char *tr = table + ((T & (kSpan - 1)) + (lane >> 2)) * kTableStride + (lane & 3) * 16;
   float lo[NR][4];
 #pragma unroll
-  for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = lo[nt][i] = 0.f;
-#pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
     uint32_t x[4], y[4];  // [key half][chunk of the k-step]: registers 0: (0, 0), 1: (1, 0), 2: (0, 1), 3: (1, 1)
     ldsm4(lbase + (((2 * ks + lch) ^ (lrow & 7)) << 4), x[0], x[1], x[2], x[3]);
@@ -117,17 +150,24 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (2 * ks + (i >> 1)) * 64);
-      const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]);
-      const float2 u = f2_get(f2_fma(Y, f2_neg(sn), f2_mul(X, cs))), v = f2_get(f2_fma(X, sn, f2_mul(Y, cs)));
+      const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]), minus = f2(-1.f, -1.f);
+      const F2 U = f2_fma(f2_mul(Y, sn), minus, f2_mul(X, cs)), V = f2_fma(X, sn, f2_mul(Y, cs));
+      const float2 u = f2_get(U), v = f2_get(V);
       uh[i] = cvt_bf16x2(u.x, u.y);
       vh[i] = cvt_bf16x2(v.x, v.y);
-      ul[i] = residue_bf16x2(u.x, u.y, uh[i]);
-      vl[i] = residue_bf16x2(v.x, v.y, vh[i]);
+      const float2 du = f2_get(f2_fma(f2_bf16(uh[i]), minus, U)), dv = f2_get(f2_fma(f2_bf16(vh[i]), minus, V));
+      ul[i] = cvt_bf16x2(du.x, du.y);
+      vl[i] = cvt_bf16x2(dv.x, dv.y);
     }
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
-      mma16816(s[nt], uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
-      mma16816(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+      if (ks == 0) {
+        mma16816_zero(s[nt], uh, qh[nt][0], qh[nt][1]);
+        mma16816_zero(lo[nt], uh, ql[nt][0], ql[nt][1]);
+      } else {
+        mma16816(s[nt], uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+      }
       mma16816(s[nt], vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
       mma16816(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
       mma16816(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
@@ -235,13 +275,13 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   Step cur = {0, 0u}, next = {0, 0u};
   if (st0 < st1) {
     cur = place(st0);
-    load_step(a.k, cur, PV || !(st0 & 1) ? sk : sv, lane);
-    if (PV) load_step(a.v, cur, sv, lane);
+    load_step(a, a.k, cur, PV || !(st0 & 1) ? sk : sv, lane);
+    if (PV) load_step(a, a.v, cur, sv, lane);
   }
   if (!PV) {
     if (st0 + 1 < st1) {
       next = place(st0 + 1);
-      load_step(a.k, next, st0 & 1 ? sk : sv, lane);
+      load_step(a, a.k, next, st0 & 1 ? sk : sv, lane);
     } else {
       cp_async_commit();
     }
@@ -308,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     if (!PV) cur = next;
     if (st + kAhead < st1) {
       next = place(st + kAhead);
-      load_step(a.k, next, keys, lane);
+      load_step(a, a.k, next, keys, lane);
     } else {
       cp_async_commit();
     }
@@ -430,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
           // The tensor cores cut their fp32 sums off instead of rounding them: over a million
           // keys an output summed there alone came out 5e-5 short.  A step's 16 keys are
           // summed there, the steps in fp32 adds that round.
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(t, v, pl[nt][0], pl[nt][1]);
+          float t[4];
+          mma16816_zero(t, v, pl[nt][0], pl[nt][1]);
           mma16816(t, v, ph[nt][0], ph[nt][1]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[PV ? nt : 0][d][i] += t[i];
@@ -439,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       }
       __syncwarp();  // the values' memory is free
       if (st + 1 < st1)
-        load_step(a.v, next, sv, lane);
+        load_step(a, a.v, next, sv, lane);
       else
         cp_async_commit();
     }
@@ -626,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int half = 0; half < 2; ++half) {
       const Step st = place_step(a, b, h, T + half * kStep, 0, len, lane);
       live[half] = st.live;
-      load_step(a.k, st, smem_u32(sm.stage[warp][half]), lane);
+      load_step(a, a.k, st, smem_u32(sm.stage[warp][half]), lane);
     }
     cp_async_wait<0>();
     __syncwarp();
