@@ -101,6 +101,16 @@ __device__ __forceinline__ void load_step(const DenseArgs &a, const uint16_t *ca
   cp_async_commit();
 }
 
+// The rotation table into shared memory (queued; the caller commits and waits).
+__device__ __forceinline__ void load_table(const DenseArgs &a, unsigned char *table, int tid) {
+  const uint32_t dst = smem_u32(table);
+#pragma unroll
+  for (int i = 0; i < kSpan * kHalf / 2 / kThreads; ++i) {
+    const int e = tid + i * kThreads;
+    cp_async16(dst + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16, ws_table(a.hdr) + 2 * e, true);
+  }
+}
+
 // 8 query rows turned by a further `delta` positions, as the B operands of the score product: each
 // value as two bf16 parts (q rounded, and what that leaves, rounded).
 template <int NR>
@@ -233,10 +243,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   RowsSmem<R> &sm = *reinterpret_cast<RowsSmem<R> *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gs = a.group_shift, G = 1 << gs, hq = a.hkv << gs;
-  if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) {
-    if (tid == 0) atomicOr(&a.hdr->err, kErrWs);
-    return;
-  }
+  const WsHeader head = *a.hdr;  // checked once the first loads are on their way
   if (MODE == 2) {  // nearly always nothing is marked
     uint32_t any = 0;
     for (int i = tid; i < kMaxShared / 4; i += kThreads) {
@@ -244,11 +251,6 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       any |= u.x | u.y | u.z | u.w;
     }
     if (!__syncthreads_or(any != 0)) return;
-  }
-  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads) {
-    const float4 w = __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
-    *reinterpret_cast<float4 *>(sm.table + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16) =
-        make_float4(w.x, w.z, w.y, w.w);
   }
   const int r = lane >> 2, c = lane & 3;
   const uint32_t sk = smem_u32(sm.stage[warp][0]), sv = sk + kStepBytes;
@@ -273,18 +275,18 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   };
   // MODE 1 has no values: its keys alternate between the two halves of the stage
   Step cur = {0, 0u}, next = {0, 0u};
+  if (work == blockIdx.x) load_table(a, sm.table, tid);  // with the first step's keys
   if (st0 < st1) {
     cur = place(st0);
     load_step(a, a.k, cur, PV || !(st0 & 1) ? sk : sv, lane);
-    if (PV) load_step(a, a.v, cur, sv, lane);
+  } else {
+    cp_async_commit();
   }
-  if (!PV) {
-    if (st0 + 1 < st1) {
-      next = place(st0 + 1);
-      load_step(a, a.k, next, st0 & 1 ? sk : sv, lane);
-    } else {
-      cp_async_commit();
-    }
+  if (st0 + (PV ? 0 : 1) < st1) {
+    if (!PV) next = place(st0 + 1);
+    load_step(a, PV ? a.v : a.k, PV ? cur : next, PV || !(st0 & 1) ? sv : sk, lane);
+  } else {
+    cp_async_commit();
   }
   if (tid < R) sm.pos[tid] = (tid >> gs) < nq ? dense_position(a, len, q0 + (tid >> gs)) : 0;
   for (int e = tid; e < R * kHalf * 2; e += kThreads) {  // query rows, turned to the tile's last position
@@ -307,7 +309,13 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     sm.q[sink][row][i] = x;
     sm.q[sink][row][i + kHalf] = y;
   }
+  cp_async_wait<1>();  // the table
   __syncthreads();
+  if (head.magic != kDenseMagic || head.rope_base != a.rope_base) {
+    cp_async_wait<0>();
+    if (tid == 0) atomicOr(&a.hdr->err, kErrWs);
+    return;
+  }
 
   // this thread's query rows: nt * 8 + 2 c + i
   float m[NR][2], l[NR][2], o[PV ? NR : 1][8][4];
@@ -647,11 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int len = dense_length(a, b, tid == 0 && split == 0 && h == 0);
-  for (int e = tid; e < kSpan * kHalf / 2; e += kThreads) {
-    const float4 w = __ldg(reinterpret_cast<const float4 *>(ws_table(a.hdr)) + e);
-    *reinterpret_cast<float4 *>(sm.table + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16) =
-        make_float4(w.x, w.z, w.y, w.w);
-  }
+  load_table(a, sm.table, tid);
+  cp_async_commit();
   const int steps = (len + 31) / 32;  // 32 keys a warp, 8 warps a round
   const int rounds = (steps + kWarps - 1) / kWarps;
   const int r = lane >> 2, c = lane & 3;
@@ -767,7 +772,9 @@ __global__ void dense_init_kernel(unsigned char *ws, double base) {
   if (r < kSpan) {
     double s, c;
     sincos((double)r * theta, &s, &c);
-    reinterpret_cast<float2 *>(ws + kDenseTable)[idx] = make_float2((float)c, (float)s);
+    float *w = reinterpret_cast<float *>(ws + kDenseTable) + (r * kHalf + (i & ~1)) * 2 + (i & 1);
+    w[0] = (float)c;  // two frequencies: cos, cos', sin, sin'
+    w[2] = (float)s;
   }
   if (r == 0) {
     const double turns = theta / (2.0 * 3.14159265358979323846);

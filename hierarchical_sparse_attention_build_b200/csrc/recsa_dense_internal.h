@@ -14,7 +14,7 @@ constexpr uint32_t kDenseMagic = 0x52534432u;  // "RSD2"
 constexpr int kSpan = 64;                      // positions of the rotation table
 constexpr int kMaxShared = 4096;               // work items whose key range may be shared by blocks
 constexpr size_t kDenseFreq = kWsHeader;                                   // uint64[64] turns
-constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float2[64][64] (cos, sin)
+constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float4[64][32] (cos, cos', sin, sin')
 constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
 constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t) + 256;  // marks of items to compute again
 constexpr size_t kDensePart = kDenseRedo + kMaxShared * sizeof(uint32_t);  // partial results
