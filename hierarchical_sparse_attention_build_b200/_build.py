@@ -15,7 +15,7 @@ LIB = os.path.join(PKG, "librecsa.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["recsa_abi.cpp", "recsa_dense_abi.cpp", "recsa_build.cu", "recsa_attend.cu", "recsa_no_alloc.cu",
-           "recsa_dense.cu", "recsa_dense_chunk.cu", "recsa_evict.cu"]
+           "recsa_dense.cu", "recsa_dense_chunk.cu", "recsa_dense_weights.cu", "recsa_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
 

@@ -1,6 +1,5 @@
 // Dense attention of a few query rows over a long cache (decode steps, short chunks, and
-// every fp32 output), the attention weight per cache slot, and token appends to a cache
-// without a tree.
+// every fp32 output), and token appends to a cache without a tree.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
 
   for (int work = blockIdx.x; work < items * a.nsplit; work += gridDim.x) {
   const int item = work / a.nsplit, split = work % a.nsplit;
-  const int tile = item % a.tiles, bh = item / a.tiles;
+  const int tile = item % a.tiles, bh = a.bh0 + item / a.tiles;
   const int b = bh / a.hkv, h = bh % a.hkv;
   const int q0 = tile * (R >> gs), nq = min(R >> gs, a.nq - q0);  // the tile's queries
   if (MODE == 2 && !redo[redo_slot(bh, chunk_tiles, q0 / (256 >> gs))]) continue;
@@ -378,6 +377,11 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
           seen[nt][i] = ((live >> key) & 1u) && t >= lo && t < hi;
           if (!seen[nt][i]) s[nt][i] = -INFINITY;
         }
+    }
+    if (MODE == 1 && a.scores && 2 * c < a.score_stride) {  // (only with 8 rows or fewer: one tile a head)
+      float *dst = a.scores + ((int64_t)(bh - a.bh0) * a.score_pitch + T + r) * a.score_stride + 2 * c;
+      *reinterpret_cast<float2 *>(dst) = make_float2(s[0][0], s[0][1]);
+      *reinterpret_cast<float2 *>(dst + 8 * a.score_stride) = make_float2(s[0][2], s[0][3]);
     }
     // Weights from the maximum so far: weights, sums and outputs hold numbers up to 2^127 with
     // the same relative precision.  Only a row whose maximum has grown by more than 2^64 (or that
@@ -627,117 +631,6 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   }
 }
 
-// ---------------------------------------------------------------------------------------
-// Weights per slot: w[t] = sum over rows of exp2(s[row][t] - lse[row]).  A block holds keys
-// (each warp 64 at a time, one span) and walks the query rows in pieces of 16; keys are
-// rotated against a span's table, rows turned to the span, so scores are formed exactly as
-// the pass that summed lse formed them.
-
-struct WeightsSmem {
-  unsigned char stage[kWarps][2][kStepBytes];  // 32 keys of a warp
-  unsigned char table[kSpan * kTableStride];
-  float q[16][kQStride];
-  float4 ang[kWarps][kHalf / 2];
-  float lse[16];
-  int pos[16];
-};
-
-__global__ void __launch_bounds__(kThreads, 1)
-    dense_weights_kernel(DenseArgs a, const float *__restrict__ lse, float *__restrict__ weights, int accumulate) {
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  WeightsSmem &sm = *reinterpret_cast<WeightsSmem *>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bh = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
-  const int b = bh / a.hkv, h = bh % a.hkv;
-  const int gs = a.group_shift, G = 1 << gs, hq = a.hkv << gs;
-  if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) {
-    if (tid == 0) atomicOr(&a.hdr->err, kErrWs);
-    return;
-  }
-  const int len = dense_length(a, b, tid == 0 && split == 0 && h == 0);
-  load_table(a, sm.table, tid);
-  cp_async_commit();
-  const int steps = (len + 31) / 32;  // 32 keys a warp, 8 warps a round
-  const int rounds = (steps + kWarps - 1) / kWarps;
-  const int r = lane >> 2, c = lane & 3;
-  const int qt = 16 >> gs;
-  float *const w_row = weights + ((int64_t)b * a.hkv + h) * a.capacity;
-
-  for (int rd = split; rd < rounds; rd += a.nsplit) {
-    const int T = (rd * kWarps + warp) * 32;
-    uint32_t live[2];
-    __syncwarp();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const Step st = place_step(a, b, h, T + half * kStep, 0, len, lane);
-      live[half] = st.live;
-      load_step(a, a.k, st, smem_u32(sm.stage[warp][half]), lane);
-    }
-    cp_async_wait<0>();
-    __syncwarp();
-    float sum[2][2] = {};  // keys r and r + 8 of each half
-    for (int q0 = 0; q0 < a.nq; q0 += qt) {
-      const int nq = min(qt, a.nq - q0);
-      const int p_max = dense_position(a, len, q0 + nq - 1);
-      __syncthreads();
-      if (tid < 16) {
-        const bool in = (tid >> gs) < nq;
-        sm.pos[tid] = in ? dense_position(a, len, q0 + (tid >> gs)) : 0;
-        sm.lse[tid] = in ? lse[((int64_t)b * a.nq + q0 + (tid >> gs)) * hq + h * G + (tid & (G - 1))] : INFINITY;
-      }
-      for (int e = tid; e < 16 * kHalf; e += kThreads) {
-        const int i = e % kHalf, row = e / kHalf;
-        float x = 0.f, y = 0.f;
-        if ((row >> gs) < nq) {
-          const uint16_t *src = a.q + (((int64_t)b * a.nq + q0 + (row >> gs)) * hq + h * G + (row & (G - 1))) * kD + i;
-          x = __uint_as_float((uint32_t)src[0] << 16) * a.qscale;
-          y = __uint_as_float((uint32_t)src[kHalf] << 16) * a.qscale;
-          const int d = dense_position(a, len, q0 + (row >> gs)) - p_max;
-          if (d != 0) {
-            const float2 w = rotation(d, __ldg(ws_freq(a.hdr) + i));
-            const float u = x * w.x - y * w.y;
-            y = y * w.x + x * w.y;
-            x = u;
-          }
-        }
-        sm.q[row][i] = x;
-        sm.q[row][i + kHalf] = y;
-      }
-      __syncthreads();
-      if (T < len && p_max > T) {
-        uint32_t qh[2][16], ql[2][16];
-        turn_queries<2>(a, sm.q, p_max - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float s[2][4];
-          const int Th = T + half * kStep;
-          score_step<2>(sm.table, smem_u32(sm.stage[warp][half]), Th, qh, ql, s, lane);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = nt * 8 + 2 * c + (i & 1);
-              if (Th + r + (i & 2) * 4 < sm.pos[row]) sum[half][i >> 1] += exp2_approx(s[nt][i] - sm.lse[row]);
-            }
-        }
-      }
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float v = sum[half][k];
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        const int key = r + 8 * k, t = T + half * kStep + key;
-        if (c == 0 && t < len) {
-          if (!((live[half] >> key) & 1u)) v = 0.f;  // a token on a page outside the pool receives nothing
-          w_row[t] = accumulate ? w_row[t] + v : v;
-        }
-      }
-  }
-}
-
 __global__ void append_tokens_kernel(DenseArgs a, uint4 *k, uint4 *v, const uint4 *__restrict__ k_new,
                                      const uint4 *__restrict__ v_new, int64_t at, int count, int64_t limit) {
   const int64_t n16 = (int64_t)a.batch * count * a.hkv * 16;
@@ -854,7 +747,7 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
   const int nr = ((int64_t)a.nq << a.group_shift) <= 8 ? 1 : 2;
   const int per = (8 * nr) >> a.group_shift;
   a.tiles = (a.nq + per - 1) / per;
-  const int64_t items = (int64_t)a.batch * a.hkv * a.tiles;
+  const int64_t items = (a.heads ? a.heads : (int64_t)a.batch * a.hkv) * a.tiles;
   a.nsplit = pick_split(items, max_keys, dense_sm_count() * blocks_per_sm(nr), 8 * nr);
   const int64_t grid = items * a.nsplit;
   if (lse)
@@ -871,17 +764,6 @@ int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream) {
   const int64_t items = (int64_t)a.batch * a.hkv * a.tiles;
   uint32_t *redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(a.hdr) + kDenseRedo);
   return run_rows<2, 2>(a, items, std::min<int64_t>(items, dense_sm_count()), nullptr, redo, chunk_tiles, stream);
-}
-
-int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream) {
-  int rc = opt_in(dense_weights_kernel, sizeof(WeightsSmem));
-  if (rc) return rc;
-  const int64_t heads = (int64_t)a.batch * a.hkv;
-  const int64_t rounds = ceil_div(a.length, 32 * kWarps);
-  a.nsplit = (int)std::min<int64_t>(std::max<int64_t>(rounds, 1), std::max<int64_t>(1, 4 * dense_sm_count() / heads));
-  dense_weights_kernel<<<(unsigned)(heads * a.nsplit), kThreads, sizeof(WeightsSmem), (cudaStream_t)stream>>>(
-      a, lse, weights, accumulate);
-  return (int)cudaGetLastError();
 }
 
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,

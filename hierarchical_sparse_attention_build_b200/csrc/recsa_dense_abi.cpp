@@ -255,9 +255,10 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
   if (rows > kMaxDenseLse) return fail(RECSA_ERR_UNSUPPORTED, "%lld query rows > %lld", (long long)rows,
                                        (long long)kMaxDenseLse);
   float *lse = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kDenseLse);
-  int rc = launch_dense_rows(a, max_keys(a), lse, stream);
-  if (rc != 0) return cuda_fail(rc, "softmax sums");
-  rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, stream);
+  const int rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, (int64_t)(ws_bytes - kDenseImages), stream);
+  if (rc == kNoRoom)
+    return fail(RECSA_ERR_UNSUPPORTED, "the rotated rows of a sequence of %lld tokens and %d queries do not fit a workspace",
+                (long long)tree->length, num_queries);
   return rc != 0 ? cuda_fail(rc, "attention weights") : RECSA_OK;
 }
 

@@ -44,6 +44,10 @@ struct DenseArgs {
   float qscale;       // softmax scale * log2(e)
   float rope_base;
   WsHeader *hdr;
+  int32_t bh0, heads;     // the rows kernel's (sequence, KV head) pairs (heads = 0: all)
+  float *scores;          // where its sums' scores go: [heads][score_pitch tokens][score_stride rows]
+  int32_t score_stride;
+  int64_t score_pitch;
 };
 
 // Mark of tile `tile` (256 query rows) of a (sequence, KV head) in the workspace's list; two tiles
@@ -61,7 +65,9 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
 constexpr int kNoRoom = -1000;
 int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, int64_t image_bytes, void *stream);
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
-int launch_dense_weights(DenseArgs a, const float *lse, float *weights, int accumulate, void *stream);
+// Weights per slot; `lse` has a float for each query row; kNoRoom, with nothing launched, where one
+// head's rotated rows do not fit `room` bytes of images.
+int launch_dense_weights(const DenseArgs &a, float *lse, float *weights, int accumulate, int64_t room, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
                          int count, int64_t limit, void *stream);
 

@@ -1,0 +1,469 @@
+// The softmax weight each cache slot receives: w[t] = sum over query rows of exp2(s[row][t] - L[row]),
+// L[row] the row's log2-sum-exp.  Every weight needs every row's sum, so the scores are needed twice.
+//
+// A few rows (a decode step: at most 8 a KV group): reading K bounds it.  The rows kernel leaves
+// its scores (4 bytes a row and key, against the key's 256) with the sums, and a second pass turns
+// them into weights: weights of one step over 4 x 65536 tokens took 394 us with K read twice.
+//
+// More rows (a prompt's last queries): the products bound it.  dense_scores_kernel forms them on
+// tcgen05 twice, with 128 x 128 tiles of keys and rows that were rotated once into shared-memory
+// images.  Pass 1 has the query rows as the product's rows, so that a thread sums a row; pass 2 has
+// the keys as rows, so that a thread sums a key over all query rows, in a fixed order and without a
+// shuffle or an atomic.  The weights are fp32, so both operands are two bf16 parts (rounded, and what
+// that leaves, rounded) and three products are summed; what is dropped is below 2^-16 of the
+// product of the magnitudes.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "recsa_dense_umma.cuh"
+
+namespace recsa {
+namespace {
+
+constexpr int kEpilogueWarps = 8;           // two sets of four, on alternate tiles
+constexpr int kScoreThreads = 320;
+constexpr int kPartBytes = 2 * kTileBytes;  // a tile's two parts
+constexpr int kMaxRange = 40;               // key tiles of a block
+constexpr int kTurnThreads = 128;
+constexpr int kTurnRows = 32;               // query rows a block of the images kernel turns
+
+struct ScoreArgs {
+  DenseArgs d;
+  int bh0, heads;              // the launch's (sequence, KV head) pairs
+  int row_tiles, key_tiles;    // of a head: 128 query rows, 128 keys
+  int nsplit;
+  unsigned char *key_images, *query_images;  // [heads][key_tiles], [heads][row_tiles]: two parts each
+  uint4 *live;                 // a key tile's tokens that were loaded
+  float2 *sums;                // [heads][row_tiles][2 nsplit][128]: a row's (maximum, sum) in part of the keys
+  float *weights;
+  int accumulate;
+};
+
+struct ScoreSmem {
+  unsigned char q[kPartBytes];
+  unsigned char k[2][kPartBytes];
+  float acc[kMaxRange * kTile];  // pass 2: the block's keys
+  alignas(16) float lse[kTile];
+  alignas(16) int pos[kTile];
+  alignas(16) uint64_t q_full;
+  uint64_t q_empty, k_full[2], k_empty[2], d_full[2], d_empty[2], drain;
+  uint32_t tmem, stop;
+};
+constexpr size_t kScoreSmem = sizeof(ScoreSmem) + 1024;
+
+// One row of 8 + 8 dimensions, turned, as two bf16 parts of a tile.
+template <bool SCALE>
+__device__ __forceinline__ void put_parts(unsigned char *tile, int row, int ch, const uint4 &lo, const uint4 &hi,
+                                          const Turn &t, float scale) {
+  const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
+  uint32_t uh[4], ul[4], vh[4], vl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    F2 p = f2_bf16(x[i]), q = f2_bf16(y[i]);
+    if (SCALE) {
+      p = f2_mul(p, f2(scale, scale));
+      q = f2_mul(q, f2(scale, scale));
+    }
+    const float2 u = f2_get(f2_fma(q, f2_neg(t.s[i]), f2_mul(p, t.c[i])));
+    const float2 v = f2_get(f2_fma(p, t.s[i], f2_mul(q, t.c[i])));
+    uh[i] = cvt_bf16x2(u.x, u.y);
+    vh[i] = cvt_bf16x2(v.x, v.y);
+    ul[i] = residue_bf16x2(u.x, u.y, uh[i]);
+    vl[i] = residue_bf16x2(v.x, v.y, vh[i]);
+  }
+  put_row(tile, row, ch, make_uint4(uh[0], uh[1], uh[2], uh[3]), make_uint4(vh[0], vh[1], vh[2], vh[3]));
+  put_row(tile + kTileBytes, row, ch, make_uint4(ul[0], ul[1], ul[2], ul[3]), make_uint4(vl[0], vl[1], vl[2], vl[3]));
+}
+
+// Query row `row` of a KV group is head row % G of query row / G.
+__device__ __forceinline__ int row_position(const DenseArgs &d, int len, int row) {
+  const int qi = row >> d.group_shift;
+  return qi < d.nq ? dense_position(d, len, qi) : 0;
+}
+
+// The first heads * key_tiles blocks turn a key tile each, the others kTurnRows query rows.
+__global__ void __launch_bounds__(kTurnThreads) dense_score_images_kernel(ScoreArgs a) {
+  const DenseArgs &d = a.d;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the score kernel reports it
+  const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
+  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
+  const int keys = a.heads * a.key_tiles;
+  if ((int)blockIdx.x >= keys) {
+    constexpr int kParts = kTile / kTurnRows;
+    const int e = blockIdx.x - keys, image = e / kParts, hl = image / a.row_tiles, rt = image % a.row_tiles;
+    const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
+    const int len = dense_length(d, b, false);
+#pragma unroll
+    for (int i = 0; i < kTurnRows / 16; ++i) {
+      const int in_tile = e % kParts * kTurnRows + r0 + 16 * i, row = rt * kTile + in_tile, qi = row >> gs;
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+      if (qi < d.nq) {
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(d.q + (((int64_t)b * d.nq + qi) * hq + h * G + (row & (G - 1))) * kD);
+        lo = __ldg(src + ch);
+        hi = __ldg(src + ch + 8);
+      }
+      Turn t;
+      t.set(f, dense_position(d, len, qi));
+      put_parts<true>(a.query_images + (int64_t)image * kPartBytes, in_tile, ch, lo, hi, t, d.qscale);
+    }
+    return;
+  }
+  const int hl = blockIdx.x / a.key_tiles, kt = blockIdx.x % a.key_tiles;
+  const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
+  const int len = dense_length(d, b, false), T = kt * kTile;
+  if (T >= len) return;
+  unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kPartBytes;
+  uint32_t word[4] = {0u, 0u, 0u, 0u};
+  uint4 xl[8], xh[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int tok = T + r0 + 16 * i;
+    xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
+    if (tok < len) {
+      const int64_t r = cache_row(d, b, h, tok);
+      if (r >= 0) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
+        xl[i] = __ldg(src + ch);
+        xh[i] = __ldg(src + ch + 8);
+        word[i >> 1] |= 1u << (r0 + 16 * (i & 1));
+      } else {
+        atomicOr(&d.hdr->err, kErrIndex);
+      }
+    }
+  }
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if ((i & 3) == 0) t.set(f, T + r0 + 16 * i);
+    put_parts<false>(tile, r0 + 16 * i, ch, xl[i], xh[i], t, 1.f);
+    if ((i & 3) != 3) {
+      Turn step;
+      step.set(f, 16);
+      t.advance(step);
+    }
+  }
+  __shared__ uint32_t words[4];
+  if (lt < 4) words[lt] = 0u;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    if (ch == 0) atomicOr(&words[w], word[w]);
+  __syncthreads();
+  if (lt == 0) a.live[blockIdx.x] = make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+// A block: a range of key tiles of one (sequence, KV head) against all its query rows, 128 at a
+// time.  Warps 0-3 and 4-7 take the products of alternate tiles from TMEM, warp 8 issues them,
+// warp 9 copies the images.
+template <int PASS>
+__global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  ScoreSmem &sm = *reinterpret_cast<ScoreSmem *>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
+  const DenseArgs &d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) {
+    if (tid == 0) atomicOr(&d.hdr->err, kErrWs);
+    return;
+  }
+  const int hl = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
+  const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
+  const int len = dense_length(d, b, PASS == 1 && tid == 0 && h == 0 && split == 0);
+  const int tiles = (len + kTile - 1) / kTile;
+  const int kt0 = (int)((int64_t)tiles * split / a.nsplit), kt1 = (int)((int64_t)tiles * (split + 1) / a.nsplit);
+  if (kt0 >= kt1) {  // pass 2 reads every block's sums
+    if (PASS == 1)
+      for (int e = tid; e < a.row_tiles * 2 * kTile; e += kScoreThreads) {
+        const int rt = e / (2 * kTile), set = e / kTile % 2;
+        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) + split * 2 + set) * kTile + e % kTile] =
+            make_float2(-INFINITY, 0.f);
+      }
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.d_full[i], 1);
+      mbar_init(&sm.d_empty[i], 4);
+    }
+    sm.stop = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) {
+    umma::tmem_alloc(&sm.tmem, 256);
+    umma::tmem_relinquish();
+  }
+  if (PASS == 2)
+    for (int i = tid; i < (kt1 - kt0) * kTile; i += kScoreThreads) sm.acc[i] = 0.f;
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  auto wait = [&](uint64_t *bar, uint32_t parity) { bounded_wait(&sm.stop, d.hdr, bar, parity); };
+  // key tiles that row tile rt's queries see (at least one, so that every row tile has a product)
+  auto last_tile = [&](int rt) {
+    const int row = min((rt + 1) * kTile, d.nq << d.group_shift) - 1;
+    const int p = row_position(d, len, row);
+    return max(kt0 + 1, min(kt1, (max(p, 0) + kTile - 1) / kTile));
+  };
+
+  if (warp < kEpilogueWarps) {
+    const int set = warp >> 2, trow = (warp & 3) * 32 + lane;
+    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + set * kTile;
+    uint32_t n = 0;  // products so far
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+      const int end = last_tile(rt);
+      if (PASS == 2) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // the last row tile's values have been read
+        if (tid < kTile) {
+          const int p = row_position(d, len, rt * kTile + tid);
+          const float2 *src = a.sums + ((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) * kTile + tid;
+          float m = -INFINITY, l = 0.f;
+          for (int j = 0; j < 2 * a.nsplit; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
+          for (int j = 0; j < 2 * a.nsplit; ++j) {
+            const float2 v = __ldcg(src + j * kTile);
+            if (v.x != -INFINITY) l += v.y * exp2_approx(v.x - m);
+          }
+          // a row that sees nothing gives no weight; neither does a row past the queries
+          sm.lse[tid] = (rt * kTile + tid) < (d.nq << d.group_shift) && (l > 0.f || l != l) ? m + log2f(l) : INFINITY;
+          sm.pos[tid] = p;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      const int p_row = PASS == 1 ? row_position(d, len, rt * kTile + trow) : 0;
+      const int p_least = row_position(d, len, rt * kTile);  // positions grow with the row
+      float m = -INFINITY, l = 0.f;
+      for (int kt = kt0; kt < end; ++kt, ++n) {
+        if ((int)(n & 1) != set) continue;
+        const int T = kt * kTile;
+        const uint4 live = __ldg(a.live + (int64_t)hl * a.key_tiles + kt);
+        wait(&sm.d_full[set], (n >> 1) & 1);
+        umma::fence_after_sync();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) umma::tmem_ld32(td + g * 32, s[g]);
+        umma::tmem_wait_ld();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.d_empty[set]);
+        if (PASS == 1) {
+          const uint32_t lv[4] = {live.x, live.y, live.z, live.w};
+          if (T + kTile > p_row || (live.x & live.y & live.z & live.w) != 0xffffffffu) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (T + g * 32 + i >= p_row || !((lv[g] >> i) & 1u)) s[g][i] = 0xff800000u;
+          }
+          float x[4] = {m, m, m, m};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) x[g] = max3(x[g], __uint_as_float(s[g][i]), __uint_as_float(s[g][i + 1]));
+          const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          if (top > m) {
+            l *= m == -INFINITY ? 0.f : exp2_approx(m - top);
+            m = top;
+          }
+          const float z = m == -INFINITY ? 0.f : m;
+          float add[4] = {};
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) add[g] += exp2_approx(__uint_as_float(s[g][i]) - z);
+          l += (add[0] + add[1]) + (add[2] + add[3]);
+        } else {
+          const int t = T + trow;
+          const uint32_t lw = trow < 32 ? live.x : trow < 64 ? live.y : trow < 96 ? live.z : live.w;
+          const bool whole = T + kTile <= p_least;
+          float add[4] = {};
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 z = *reinterpret_cast<const float4 *>(&sm.lse[g * 32 + i]);
+              float e[4] = {exp2_approx(__uint_as_float(s[g][i]) - z.x), exp2_approx(__uint_as_float(s[g][i + 1]) - z.y),
+                            exp2_approx(__uint_as_float(s[g][i + 2]) - z.z),
+                            exp2_approx(__uint_as_float(s[g][i + 3]) - z.w)};
+              if (!whole) {
+                const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 32 + i]);
+                if (t >= p.x) e[0] = 0.f;
+                if (t >= p.y) e[1] = 0.f;
+                if (t >= p.z) e[2] = 0.f;
+                if (t >= p.w) e[3] = 0.f;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) add[k] += e[k];
+            }
+          if ((lw >> (trow & 31)) & 1u) sm.acc[(kt - kt0) * kTile + trow] += (add[0] + add[1]) + (add[2] + add[3]);
+        }
+      }
+      if (PASS == 1)
+        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) + split * 2 + set) * kTile + trow] = make_float2(m, l);
+    }
+    if (PASS == 2) {
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      float *const w = a.weights + ((int64_t)b * d.hkv + h) * d.capacity;
+      for (int t = kt0 * kTile + tid; t < min(kt1 * kTile, len); t += kEpilogueWarps * 32) {
+        const float v = sm.acc[t - kt0 * kTile];
+        w[t] = a.accumulate ? w[t] + v : v;
+      }
+    }
+  } else if (warp == 8) {
+    if (elect_one()) {
+      const uint64_t dq = swizzled_desc(smem_u32(sm.q), 16), dk = swizzled_desc(smem_u32(sm.k[0]), 16);
+      uint32_t n = 0;
+      for (int rt = 0; rt < a.row_tiles; ++rt) {
+        const int end = last_tile(rt);
+        wait(&sm.q_full, rt & 1);
+        for (int kt = kt0; kt < end; ++kt, ++n) {
+          const uint32_t s = n & 1;
+          wait(&sm.k_full[s], (n >> 1) & 1);
+          if (n >= 2) wait(&sm.d_empty[s], ((n >> 1) - 1) & 1);
+          umma::fence_after_sync();
+          const uint64_t k = dk + s * (kPartBytes >> 4);
+          const uint64_t rows = PASS == 1 ? dq : k, cols = PASS == 1 ? k : dq;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {  // small terms first: low x high, high x low, high x high
+            const uint64_t ra = rows + (p == 0 ? kTileBytes >> 4 : 0), cb = cols + (p == 1 ? kTileBytes >> 4 : 0);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+              umma::mma(tmem + s * kTile, ra + off, cb + off, chunk_idesc(kTile, true, false), p + ks > 0);
+            }
+          }
+          umma::commit(&sm.d_full[s]);
+          umma::commit(&sm.k_empty[s]);
+        }
+        umma::commit(&sm.q_empty);
+      }
+      umma::commit(&sm.drain);  // nothing may be in flight when the tensor memory is freed
+      if (!mbar_wait(&sm.drain, 0)) atomicOr(&d.hdr->err, kErrTimeout);
+    }
+  } else if (elect_one()) {
+    uint32_t n = 0;
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+      const int end = last_tile(rt);
+      if (rt > 0) wait(&sm.q_empty, (rt - 1) & 1);
+      mbar_expect(&sm.q_full, kPartBytes);
+      bulk_load(smem_u32(sm.q), a.query_images + ((int64_t)hl * a.row_tiles + rt) * kPartBytes, kPartBytes, &sm.q_full);
+      for (int kt = kt0; kt < end; ++kt, ++n) {
+        const uint32_t s = n & 1;
+        if (n >= 2) wait(&sm.k_empty[s], ((n >> 1) - 1) & 1);
+        mbar_expect(&sm.k_full[s], kPartBytes);
+        bulk_load(smem_u32(sm.k[s]), a.key_images + ((int64_t)hl * a.key_tiles + kt) * kPartBytes, kPartBytes,
+                  &sm.k_full[s]);
+      }
+    }
+    // every copy has landed before the block may end
+    for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(&sm.k_full[i & 1], (i >> 1) & 1);
+  }
+  __syncwarp();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 8) umma::tmem_dealloc(tmem, 256);
+}
+
+// Weights from the scores that the rows kernel left: a thread a key.
+__global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, const float *__restrict__ lse,
+                                                                 float *__restrict__ weights, int accumulate) {
+  if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) return;  // the rows kernel reported it
+  const int bh = a.bh0 + blockIdx.y, b = bh / a.hkv, h = bh % a.hkv, gs = a.group_shift, G = 1 << gs;
+  const int len = dense_length(a, b, false), rows = a.nq << gs;
+  __shared__ float z[8];
+  if (threadIdx.x < 8)
+    z[threadIdx.x] = threadIdx.x < rows ? lse[((int64_t)b * a.nq + (threadIdx.x >> gs)) * (a.hkv << gs) + h * G +
+                                              (threadIdx.x & (G - 1))]
+                                        : INFINITY;
+  __syncthreads();
+  const float *s = a.scores + (int64_t)blockIdx.y * a.score_pitch * a.score_stride;
+  float *const w = weights + ((int64_t)b * a.hkv + h) * a.capacity;
+  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < len; t += gridDim.x * blockDim.x) {
+    float v = 0.f;
+    for (int i = 0; i < a.score_stride; i += 2) {
+      const float2 x = __ldcs(reinterpret_cast<const float2 *>(s + (int64_t)t * a.score_stride + i));
+      if (i < rows) v += exp2_approx(x.x - z[i]);
+      if (i + 1 < rows) v += exp2_approx(x.y - z[i + 1]);
+    }
+    w[t] = accumulate ? w[t] + v : v;
+  }
+}
+
+int few_rows(DenseArgs d, float *lse, float *weights, int accumulate, int64_t room, void *stream) {
+  const int64_t heads = (int64_t)d.batch * d.hkv;
+  const int rows = d.nq << d.group_shift;
+  d.score_stride = rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
+  d.score_pitch = ceil_div(std::max(d.length, 1), 16) * 16;
+  const int64_t fit = std::min<int64_t>(room / (d.score_pitch * d.score_stride * (int64_t)sizeof(float)), 65535);
+  if (fit < 1) return kNoRoom;
+  d.scores = reinterpret_cast<float *>(reinterpret_cast<char *>(d.hdr) + kDenseImages);
+  const int64_t step = std::min(heads, fit);
+  for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
+    d.bh0 = (int)bh0;
+    d.heads = (int)std::min(step, heads - bh0);
+    const int rc = launch_dense_rows(d, d.length, lse, stream);
+    if (rc) return rc;
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(d.score_pitch, 256), 4096), (unsigned)d.heads);
+    weights_from_scores_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(d, lse, weights, accumulate);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return (int)e;
+  }
+  return 0;
+}
+
+}  // namespace
+
+int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int accumulate, int64_t room, void *stream) {
+  const int64_t rows = (int64_t)d.nq << d.group_shift, heads = (int64_t)d.batch * d.hkv;
+  if (rows <= 8) {
+    const int rc = few_rows(d, lse, weights, accumulate, room, stream);
+    if (rc != kNoRoom) return rc;
+  }
+  ScoreArgs a = {};
+  a.d = d;
+  a.weights = weights;
+  a.accumulate = accumulate;
+  a.row_tiles = (int)ceil_div(rows, kTile);
+  a.key_tiles = (int)ceil_div(std::max(d.length, 1), kTile);
+  const int64_t head_bytes = a.key_tiles * (int64_t)(kPartBytes + sizeof(uint4)) + a.row_tiles * (int64_t)kPartBytes;
+  const int64_t fit = room / head_bytes;
+  if (fit < 1) return kNoRoom;
+  cudaError_t e = cudaFuncSetAttribute(dense_scores_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dense_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
+  if (e != cudaSuccess) return (int)e;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int sms = dense_sm_count();
+  // the sums of a head's rows, once for each part of the keys
+  const int64_t least = ceil_div(a.key_tiles, kMaxRange);
+  const int64_t sums_room = (int64_t)kDensePartBytes / (a.row_tiles * 2 * (int64_t)(kTile * sizeof(float2)));
+  if (sums_room < least) return kNoRoom;
+  const int64_t step = std::min({heads, fit, sums_room / least});
+  for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
+    a.bh0 = (int)bh0;
+    a.heads = (int)std::min(step, heads - bh0);
+    // one wave of blocks where that leaves each at most kMaxRange key tiles
+    a.nsplit = (int)std::min<int64_t>({std::max<int64_t>(least, sms / a.heads), a.key_tiles, sums_room / a.heads});
+    a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
+    a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kPartBytes;
+    a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * a.row_tiles * kPartBytes);
+    a.sums = reinterpret_cast<float2 *>(reinterpret_cast<char *>(d.hdr) + kDensePart);
+    const int64_t blocks = (int64_t)a.heads * (a.key_tiles + (int64_t)a.row_tiles * (kTile / kTurnRows));
+    dense_score_images_kernel<<<(unsigned)blocks, kTurnThreads, 0, st>>>(a);
+    dense_scores_kernel<1><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
+    dense_scores_kernel<2><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return (int)e;
+  }
+  return 0;
+}
+
+}  // namespace recsa

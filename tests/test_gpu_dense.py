@@ -433,6 +433,10 @@ def test_chunk_rows_beyond_half_precision():
     (3, 2, 2, 65, 80, 0, [65, 10, 33], dict(causal=True, own=True)),
     (1, 8, 4, 2500, 64, 64, None, dict(causal=True, own=True)),
     (2, 1, 4, 5000, 2, 0, None, {}),
+    (2, 2, 1, 777, 1, 64, [777, 5], {}),
+    (1, 2, 2, 6000, 600, 0, None, dict(causal=True, own=True)),
+    (3, 2, 8, 900, 33, 16, [900, 0, 20], dict(causal=True, own=True)),
+    (1, 1, 1, 200, 9, 0, None, {}),
 ])
 def test_weights(B, H, G, L, n, page, lens, view):
     c = Case(B, H, G, L, n, seed=L + n, page=page, lens=lens, spare=7)
