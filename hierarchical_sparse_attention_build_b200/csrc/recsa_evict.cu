@@ -21,13 +21,14 @@ namespace cg = cooperative_groups;
 namespace recsa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxBlocks = 8;   // of a cluster
 
 struct SelectSmem {
   int hist[3][kBins];
-  int warp_gt[kSelWarps], warp_eq[kSelWarps];
+  int warp_gt[kSelWarps], warp_eq[kSelWarps];  // then: of the warps before
   int gt, eq;          // this block's totals
   int digit, above;    // the digit found, and how many keys lie above it
   int scan[kSelWarps];
@@ -36,7 +37,9 @@ struct SelectSmem {
 // larger weight -> larger key; NaN below every number
 __device__ __forceinline__ uint32_t weight_key(float w) { return w == w ? order_key(w) : 0u; }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs a) {
+// PER > 0: a thread holds its weights' keys, at most PER of them; 0: they are read again each time.
+template <int PER>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelectSmem &sm = *reinterpret_cast<SelectSmem *>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -58,6 +61,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
   const int64_t span = (int64_t)(f1 - f0 + 31) / 32, parts = (int64_t)nblk * kSelWarps, part = rank * kSelWarps + warp;
   const int w0 = f0 + (int)(span * part / parts) * 32, w1 = min(f1, f0 + (int)(span * (part + 1) / parts) * 32);
 
+  uint32_t held[PER ? PER : 1];
+  if (PER) {
+    float x[PER ? PER : 1];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) x[j] = w0 + lane + 32 * j < w1 ? __ldg(w + w0 + lane + 32 * j) : 0.f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) held[j] = weight_key(x[j]);
+  }
+  // f(slot, key) for each of this lane's slots
+  auto each = [&](auto &&f) {
+    if (PER) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (w0 + lane + 32 * j < w1) f(w0 + lane + 32 * j, held[j]);
+    } else {
+#pragma unroll 8
+      for (int i = w0 + lane; i < w1; i += 32) f(i, weight_key(__ldg(w + i)));
+    }
+  };
   uint32_t floor_key = 0xffffffffu;  // the smallest kept key (none: want = 0)
   int left = want;                   // how many keys equal to it stay
   if (want > 0) {
@@ -66,22 +88,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
       const uint32_t mask = d == 2 ? 1023u : 2047u;
-#pragma unroll 4
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t key = weight_key(__ldg(w + i));
+      each([&](int, uint32_t key) {
         const bool in = d == 0 || (d == 1 ? (key >> 21) == prefix : (key >> 10) == prefix);
         if (in) atomicAdd(&sm.hist[d][(key >> shift) & mask], 1);
-      }
+      });
       cluster.sync();
-      // bins from the top: thread t sums bins kBins-1-2t and kBins-2-2t over the cluster
-      int c0 = 0, c1 = 0;
-      const int top = kBins - 1 - 2 * tid;
-      for (int k = 0; k < nblk; ++k) {
-        const int *h = cluster.map_shared_rank(&sm.hist[d][0], k);
-        c0 += h[top];
-        c1 += h[top - 1];
-      }
-      int incl = c0 + c1;
+      // bins from the top: thread t sums bins kBins-1-4t down to kBins-4-4t over the cluster
+      constexpr int kPer = kBins / kSelThreads;
+      static_assert(kPer == 4, "a thread's bins are one 16-byte load");
+      const int top = kBins - 1 - kPer * tid;
+      int4 part[kMaxBlocks];
+#pragma unroll
+      for (int k = 0; k < kMaxBlocks; ++k)
+        part[k] = k < nblk ? *reinterpret_cast<const int4 *>(cluster.map_shared_rank(&sm.hist[d][top - 3], k))
+                           : make_int4(0, 0, 0, 0);
+      int c[kPer] = {0, 0, 0, 0};  // the highest bin first
+#pragma unroll
+      for (int k = 0; k < kMaxBlocks; ++k) c[0] += part[k].w, c[1] += part[k].z, c[2] += part[k].y, c[3] += part[k].x;
+      const int own = c[0] + c[1] + c[2] + c[3];
+      int incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -89,10 +114,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
       }
       if (lane == 31) sm.scan[warp] = incl;
       __syncthreads();
-      int before = incl - c0 - c1;
-      for (int k = 0; k < warp; ++k) before += sm.scan[k];
-      if (before < left && before + c0 >= left) sm.digit = top, sm.above = before;
-      if (before + c0 < left && before + c0 + c1 >= left) sm.digit = top - 1, sm.above = before + c0;
+      const int before_warp = warp_sum_int(lane < warp ? sm.scan[lane] : 0);
+      int before = before_warp + incl - own;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (before < left && before + c[i] >= left) sm.digit = top - i, sm.above = before;
+        before += c[i];
+      }
       __syncthreads();
       prefix = d == 0 ? (uint32_t)sm.digit : d == 1 ? (prefix << 11) | (uint32_t)sm.digit
                                                     : (prefix << 10) | (uint32_t)sm.digit;
@@ -103,12 +131,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
   }
   // how many larger and equal keys each warp holds, then each block's place in slot order
   int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = weight_key(__ldg(w + i));
+  each([&](int, uint32_t key) {
     gt += key > floor_key;
     eq += key == floor_key;
-  }
+  });
   gt = warp_sum_int(gt);
   eq = warp_sum_int(eq);
   if (lane == 0) sm.warp_gt[warp] = gt, sm.warp_eq[warp] = eq;
@@ -120,12 +146,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     sm.eq = e;
   }
   cluster.sync();
-  gt = eq = 0;
-  for (int k = 0; k < rank; ++k) gt += *cluster.map_shared_rank(&sm.gt, k), eq += *cluster.map_shared_rank(&sm.eq, k);
-  for (int k = 0; k < warp; ++k) gt += sm.warp_gt[k], eq += sm.warp_eq[k];
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < w1 ? weight_key(__ldg(w + i)) : 0u;
+  gt = lane < rank ? *cluster.map_shared_rank(&sm.gt, lane) : 0;
+  eq = lane < rank ? *cluster.map_shared_rank(&sm.eq, lane) : 0;
+  if (lane < warp) gt += sm.warp_gt[lane], eq += sm.warp_eq[lane];
+  gt = warp_sum_int(gt);
+  eq = warp_sum_int(eq);
+  auto write = [&](int i, uint32_t key) {
     const bool is_gt = i < w1 && key > floor_key, is_eq = i < w1 && key == floor_key && left > 0;
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
@@ -134,6 +160,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     if (is_gt || (is_eq && e < left)) kept[at] = i;
     gt += __popc(mg);
     eq += __popc(me);
+  };
+  if (PER) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) write(w0 + lane + 32 * j, held[j]);
+  } else {
+#pragma unroll 8
+    for (int i0 = w0; i0 < w1; i0 += 32) write(i0 + lane, i0 + lane < w1 ? weight_key(__ldg(w + i0 + lane)) : 0u);
   }
   if (rank == 0) {
     for (int j = tid; j < a.sinks; j += kSelThreads) kept[j] = j;
@@ -143,7 +176,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
 }
 
 // Rows to another cache: nothing overlaps, 16 threads a row.
-__global__ void evict_copy_kernel(EvictArgs a) {
+__global__ void evict_copy_kernel(EvictArgs a, int64_t *to_len) {
+  if (to_len && blockIdx.x == 0)  // the receiving cache's lengths
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) to_len[b] = min(evict_length(a, b), a.keep);
   const int64_t rows = (int64_t)a.batch * a.hkv * a.keep;
   const int part = threadIdx.x & 15;
   for (int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 4; e < rows;
@@ -220,7 +255,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
   }
 }
 
-// after the rows: the receiving cache's per-sequence lengths
+// in place, after the rows: the per-sequence lengths
 __global__ void evict_lengths_kernel(EvictArgs a, int64_t *to_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b < a.batch) to_len[b] = min(evict_length(a, b), a.keep);
@@ -232,7 +267,7 @@ int launch_evict(const EvictArgs &a, bool in_place, int64_t *to_len, void *strea
   const cudaStream_t st = (cudaStream_t)stream;
   const int64_t heads = (int64_t)a.batch * a.hkv;
   cudaLaunchConfig_t cfg = {};
-  const int blocks = a.length > 8192 ? 8 : 1;
+  const int blocks = a.length > 8192 ? kMaxBlocks : 1;
   cfg.gridDim = dim3((unsigned)(heads * blocks));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = sizeof(SelectSmem);
@@ -243,21 +278,25 @@ int launch_evict(const EvictArgs &a, bool in_place, int64_t *to_len, void *strea
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  // a thread's slots, as the kernel deals them out: whole 32s a warp
+  const int64_t per = ceil_div(ceil_div(a.length, 32), (int64_t)blocks * kSelWarps);
+  cudaError_t e = per <= 4    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, a)
+                  : per <= 8  ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, a)
+                  : per <= 16 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, a)
+                  : per <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, a)
+                              : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, a);
   if (e != cudaSuccess) return (int)e;
   if (in_place) {
     evict_move_kernel<<<(unsigned)(heads * 9), kMoveThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !to_len) return (int)e;
+    evict_lengths_kernel<<<(unsigned)ceil_div(a.batch, 128), 128, 0, st>>>(a, to_len);
   } else {
     const int64_t threads = heads * a.keep * 16;
     const int64_t grid = std::min<int64_t>(ceil_div(threads, 256), (int64_t)dense_sm_count() * 16);
-    evict_copy_kernel<<<(unsigned)grid, 256, 0, st>>>(a);
+    evict_copy_kernel<<<(unsigned)grid, 256, 0, st>>>(a, to_len);
   }
   e = cudaGetLastError();
-  if (e != cudaSuccess) return (int)e;
-  if (to_len) {
-    evict_lengths_kernel<<<(unsigned)ceil_div(a.batch, 128), 128, 0, st>>>(a, to_len);
-    e = cudaGetLastError();
-  }
   return (int)e;
 }
 
