@@ -104,6 +104,8 @@ __device__ __forceinline__ Item chunk_item(const ChunkArgs &a, int item) {
   it.tiles = max(1, it.n1 + (it.hi2 > it.lo2 ? (it.hi2 + kTile - 1) / kTile - it.first : 0));
   return it;
 }
+// Whether the item's rows reach into its second row tile.
+__device__ __forceinline__ bool two_tiles(const DenseArgs &d, const Item &it) { return (it.nq << d.group_shift) > kTile; }
 // Where the rows kernel looks whether to compute a tile of the chunk again.
 __device__ __forceinline__ void mark_again(const ChunkArgs &a, int b, int h, int tile) {
   a.redo[redo_slot(b * a.d.hkv + h, a.d.tiles, tile)] = 1u;
@@ -203,7 +205,7 @@ __device__ __forceinline__ bool beyond_half(__half2 most) {
 
 // Rotated keys (the first `keys` blocks: a key tile each) and queries (kQueryRows rows a block)
 // of a launch as the chunk kernel's images.
-__global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a, int keys) {
+__global__ void __launch_bounds__(kLoadThreads, 6) dense_images_kernel(ChunkArgs a, int keys) {
   const DenseArgs &d = a.d;
   if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the chunk kernel reports it
   const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3;
@@ -225,33 +227,36 @@ __global__ void __launch_bounds__(kLoadThreads) dense_images_kernel(ChunkArgs a,
   const int T = (kt < hr.n1 ? kt : hr.first + kt - hr.n1) * kTile;
   unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kTileBytes;
   uint32_t word[4] = {0u, 0u, 0u, 0u};
-  uint4 xl[8], xh[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int tok = T + r0 + 16 * i;
-    xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
-    if (tok < len) {
-      const int64_t r = cache_row(d, b, h, tok);
-      if (r >= 0) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
-        xl[i] = __ldg(src + ch);
-        xh[i] = __ldg(src + ch + 8);
-        word[i >> 1] |= 1u << (r0 + 16 * (i & 1));
-      } else {
-        atomicOr(&d.hdr->err, kErrIndex);
-      }
-    }
-  }
   Turn t, step;
   const uint64_t *f = ws_freq(d.hdr) + ch * 8;
   t.set(f, T + r0);
   step.set(f, 16);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint4 ol, oh;
-    turn_row<false>(xl[i], xh[i], t, 1.f, ol, oh, most);
-    put_row(tile, r0 + 16 * i, ch, ol, oh);
-    t.advance(step);
+  for (int i0 = 0; i0 < 8; i0 += 4) {  // four rows in flight
+    uint4 xl[4], xh[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = T + r0 + 16 * (i0 + i);
+      xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
+      if (tok < len) {
+        const int64_t r = cache_row(d, b, h, tok);
+        if (r >= 0) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
+          xl[i] = __ldg(src + ch);
+          xh[i] = __ldg(src + ch + 8);
+          word[(i0 + i) >> 1] |= 1u << (r0 + 16 * (i & 1));
+        } else {
+          atomicOr(&d.hdr->err, kErrIndex);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 ol, oh;
+      turn_row<false>(xl[i], xh[i], t, 1.f, ol, oh, most);
+      put_row(tile, r0 + 16 * (i0 + i), ch, ol, oh);
+      t.advance(step);
+    }
   }
   __shared__ uint32_t words[4];
   if (lt < 4) words[lt] = 0u;
@@ -375,6 +380,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
     const int row = t * kTile + trow, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
     uint32_t n = 0, n_s = 0, n_join = 0;  // key tiles seen; phases of s_full and join
     while (segments_next(a, sm, sg, it)) {
+      const bool busy = t == 0 || two_tiles(d, it);
       const bool in = (row >> gs) < it.nq;
       const int p = in ? dense_position(d, it.len, it.q0 + (row >> gs)) : INT_MAX;  // rows past the chunk: no mask
       const int lo = in ? window_first(d, p) : 0, hi_sink = min(p, it.hi1);
@@ -382,7 +388,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       const int lo_all = __reduce_max_sync(0xffffffffu, lo), hi_all = __reduce_min_sync(0xffffffffu, p),
                 hi_sink_all = __reduce_min_sync(0xffffffffu, hi_sink);
       float m = -INFINITY, l = 0.f;
-      for (int j = sg.j0; j < sg.j1; ++j, ++n, ++n_s) {
+      if (!busy) n += sg.j1 - sg.j0;
+      for (int j = sg.j0; busy && j < sg.j1; ++j, ++n, ++n_s) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int T = it.token(j) + h * kStepKeys;
@@ -440,10 +447,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
         }
       }
       // s_full arrives once more after the segment's last products
-      wait(sm, a, &sm.s_full[t][0], n_s & 1);
-      wait(sm, a, &sm.s_full[t][1], n_s & 1);
-      ++n_s;
-      umma::fence_after_sync();
+      if (busy) {
+        wait(sm, a, &sm.s_full[t][0], n_s & 1);
+        wait(sm, a, &sm.s_full[t][1], n_s & 1);
+        ++n_s;
+        umma::fence_after_sync();
+      }
       // epilogue: the item's output, or this block's part of it: [32 pieces of 16 bytes][row], then
       // (maximum, sum) [row]
       const bool part = sg.j1 - sg.j0 < it.tiles;
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       bool odd = !(l < INFINITY);
       float *const mypart = part_of(blockIdx.x, sg.at - (sg.j1 - sg.j0) == sg.begin);
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; busy && g < 4; ++g) {
         uint32_t o[32];
         umma::tmem_ld32(to + g * 32, o);
         umma::tmem_wait_ld();
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       }
       umma::fence_before_sync();
       if (part) {
-        reinterpret_cast<float2 *>(mypart + kItemRows * kD)[row] = make_float2(m, l);
+        if (busy) reinterpret_cast<float2 *>(mypart + kItemRows * kD)[row] = make_float2(m, l);
         odd = false;
         // the item's key tiles are spread over blocks c0 .. c1: the last to arrive joins them in order
         const int total = sm.prefix[a.items], blocks = sharing_blocks(total);
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
         wait(sm, a, &sm.joined, n_join & 1);
         ++n_join;
         __threadfence();
-        if (sm.last) {
+        if (sm.last && busy) {
           // the item is in block c's first segment if the block begins inside it
           auto from = [&](int c) { return part_of(c, dealt(total, blocks, c) >= w0); };
           auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(from(c) + kItemRows * kD) + row); };
@@ -627,7 +636,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       const uint32_t ts = tmem + t * kTile, to = tmem + 2 * kTile + t * kTile;
       const uint64_t dq = swizzled_desc(smem_u32(sm.q[t]), 16), dk = swizzled_desc(smem_u32(sm.k[0]), 16),
                      dv = swizzled_desc(smem_u32(sm.v[0]), kHalfBytes);
-      uint32_t n = 0;  // key tiles
+      uint32_t n = 0, n_p = 0;  // key tiles; phases of p_full
       auto scores = [&](int h, uint32_t i) {
         const uint64_t k = dk + (i % kRing) * (kTileBytes >> 4) + h * ((kStepKeys * 128) >> 4);
 #pragma unroll
@@ -638,6 +647,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       };
       while (segments_next(a, sm, sg, it)) {
         const int count = sg.j1 - sg.j0;
+        if (t == 1 && !two_tiles(d, it)) {  // the other row tile holds all rows: tiles are let go as they come
+          for (int j = 0; j < count; ++j, ++n) {
+            wait(sm, a, &sm.k_full[n % kRing], (n / kRing) & 1);
+            umma::commit(&sm.k_empty[n % kRing]);
+            wait(sm, a, &sm.v_full[n % kRing], (n / kRing) & 1);
+            umma::commit(&sm.v_empty[n % kRing]);
+          }
+          continue;
+        }
         wait(sm, a, &sm.k_full[n % kRing], (n / kRing) & 1);
         umma::fence_after_sync();
 #pragma unroll
@@ -646,14 +664,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
           umma::commit(&sm.s_full[t][h]);
         }
         umma::commit(&sm.k_empty[n % kRing]);
-        for (int j = 0; j < count; ++j, ++n) {
+        for (int j = 0; j < count; ++j, ++n, ++n_p) {
           const uint32_t s = n % kRing, s1 = (n + 1) % kRing;
           const bool more = j + 1 < count;
           wait(sm, a, &sm.v_full[s], (n / kRing) & 1);
           if (more) wait(sm, a, &sm.k_full[s1], ((n + 1) / kRing) & 1);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            wait(sm, a, &sm.p_full[t][h], n & 1);
+            wait(sm, a, &sm.p_full[t][h], n_p & 1);
             umma::fence_after_sync();
             const uint64_t v = dv + s * (kTileBytes >> 4) + h * ((kStepKeys * 128) >> 4);
 #pragma unroll

@@ -85,7 +85,7 @@ __device__ __forceinline__ int row_position(const DenseArgs &d, int len, int row
 }
 
 // The first heads * key_tiles blocks turn a key tile each, the others kTurnRows query rows.
-__global__ void __launch_bounds__(kTurnThreads) dense_score_images_kernel(ScoreArgs a) {
+__global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(ScoreArgs a) {
   const DenseArgs &d = a.d;
   if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the score kernel reports it
   const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
@@ -118,31 +118,32 @@ __global__ void __launch_bounds__(kTurnThreads) dense_score_images_kernel(ScoreA
   if (T >= len) return;
   unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kPartBytes;
   uint32_t word[4] = {0u, 0u, 0u, 0u};
-  uint4 xl[8], xh[8];
+  Turn t, step;
+  t.set(f, T + r0);
+  step.set(f, 16);
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8; i0 += 4) {  // four rows in flight
+    uint4 xl[4], xh[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int tok = T + r0 + 16 * i;
-    xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
-    if (tok < len) {
-      const int64_t r = cache_row(d, b, h, tok);
-      if (r >= 0) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
-        xl[i] = __ldg(src + ch);
-        xh[i] = __ldg(src + ch + 8);
-        word[i >> 1] |= 1u << (r0 + 16 * (i & 1));
-      } else {
-        atomicOr(&d.hdr->err, kErrIndex);
+    for (int i = 0; i < 4; ++i) {
+      const int tok = T + r0 + 16 * (i0 + i);
+      xl[i] = xh[i] = make_uint4(0, 0, 0, 0);
+      if (tok < len) {
+        const int64_t r = cache_row(d, b, h, tok);
+        if (r >= 0) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(d.k + r * kD);
+          xl[i] = __ldg(src + ch);
+          xh[i] = __ldg(src + ch + 8);
+          word[i >> 1] |= i0 ? 0u : 1u << (r0 + 16 * (i & 1));
+          word[2 + (i >> 1)] |= i0 ? 1u << (r0 + 16 * (i & 1)) : 0u;
+        } else {
+          atomicOr(&d.hdr->err, kErrIndex);
+        }
       }
     }
-  }
-  Turn t;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if ((i & 3) == 0) t.set(f, T + r0 + 16 * i);
-    put_parts<false>(tile, r0 + 16 * i, ch, xl[i], xh[i], t, 1.f);
-    if ((i & 3) != 3) {
-      Turn step;
-      step.set(f, 16);
+    for (int i = 0; i < 4; ++i) {
+      put_parts<false>(tile, r0 + 16 * (i0 + i), ch, xl[i], xh[i], t, 1.f);
       t.advance(step);
     }
   }
