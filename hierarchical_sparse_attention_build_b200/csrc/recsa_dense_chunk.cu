@@ -270,6 +270,9 @@ __global__ void __launch_bounds__(kLoadThreads, 6) dense_images_kernel(ChunkArgs
     for (int i = 0; i < d.tiles; ++i) mark_again(a, b, h, i);
 }
 
+// bits n .. 31 (none for n >= 32, all for n <= 0)
+__device__ __forceinline__ uint32_t bits_from(int n) { return n >= 32 ? 0u : 0xffffffffu << max(n, 0); }
+
 __device__ __forceinline__ float row_max(const uint32_t (&s)[2][32]) {
   float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -406,10 +409,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
             const uint2 live = reinterpret_cast<const uint2 *>(&sm.live[n & 3])[h];
             const int a0 = (sink ? 0 : lo) - T, a1 = (sink ? hi_sink : p) - T;  // visible columns [a0, a1)
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t seen = (g ? live.y : live.x) & bits_from(a0 - 32 * g) & ~bits_from(a1 - 32 * g);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (g * 32 + i < a0 || g * 32 + i >= a1 || !(((g ? live.y : live.x) >> i) & 1u)) s[g][i] = 0xff800000u;
+                if (!((seen >> i) & 1u)) s[g][i] = 0xff800000u;
+            }
           }
           const bool first = j == sg.j0 && h == 0;
           if (first) m = row_max(s);
@@ -528,21 +533,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
           }
           const float iv = ll == 0.f ? 0.f : 1.f / ll;
           odd = !(ll < INFINITY);
+          auto factor = [&](float mc) { return mc == -INFINITY ? 0.f : exp2_approx(mc - mm) * iv; };
 #pragma unroll 1
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 4; ++g) {  // 32 dimensions, two parts in flight
             float acc[32] = {};
-            for (int c = c0; c <= c1; ++c) {
-              const float mc = stats(c).x;
-              const float4 *src = reinterpret_cast<const float4 *>(from(c)) + g * 8 * kItemRows + row;
-              float4 u[8];
+#pragma unroll 1
+            for (int c = c0; c <= c1; c += 2) {
+              const bool two = c < c1;
+              const float *pa = from(c), *pb = two ? from(c + 1) : pa;
+              const float4 *sa = reinterpret_cast<const float4 *>(pa) + g * 8 * kItemRows + row;
+              const float4 *sb = reinterpret_cast<const float4 *>(pb) + g * 8 * kItemRows + row;
+              const float ma = stats(c).x, mb = two ? stats(c + 1).x : -INFINITY;
+              float4 u[8], v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) u[i] = __ldcg(src + i * kItemRows);
-              if (mc == -INFINITY) continue;
-              const float f = exp2_approx(mc - mm) * iv;
+              for (int i = 0; i < 8; ++i) u[i] = __ldcg(sa + i * kItemRows);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = two ? __ldcg(sb + i * kItemRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float fa = factor(ma), fb = factor(mb);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                acc[4 * i] += f * u[i].x, acc[4 * i + 1] += f * u[i].y;
-                acc[4 * i + 2] += f * u[i].z, acc[4 * i + 3] += f * u[i].w;
+                acc[4 * i] += fa * u[i].x + fb * v[i].x, acc[4 * i + 1] += fa * u[i].y + fb * v[i].y;
+                acc[4 * i + 2] += fa * u[i].z + fb * v[i].z, acc[4 * i + 3] += fa * u[i].w + fb * v[i].w;
               }
             }
 #pragma unroll
