@@ -317,13 +317,17 @@ def check_device_errors(ws: Workspace, stream=None) -> None:
 # --------------------------------------------------------------------------- dense operators
 
 
+DENSE_AUTO, DENSE_ROWS, DENSE_CHUNK = 0, 1, 2
+
+
 class View(ctypes.Structure):
     """recsa_view: which tokens a dense query sees.
 
     window = 0 sees every token before the query; otherwise the last `window` tokens and the
     first `sinks`.  causal: the queries belong to the cache's last tokens (else all sit at its
     end); own_token: a causal query also sees its own token.  token_positions: sinks outside
-    the window are scored at their token positions instead of their rank among the visible."""
+    the window are scored at their token positions instead of their rank among the visible.
+    kernel: DENSE_AUTO, DENSE_ROWS or DENSE_CHUNK."""
 
     _fields_ = [
         ("sinks", ctypes.c_int32),
@@ -331,12 +335,12 @@ class View(ctypes.Structure):
         ("sink_positions", ctypes.c_int32),
         ("causal", ctypes.c_int32),
         ("own_token", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("kernel", ctypes.c_int32),
     ]
 
     def __init__(self, sinks: int = 0, window: int = 0, causal: bool = False, own_token: bool = False,
-                 token_positions: bool = False):
-        super().__init__(sinks, window, int(token_positions), int(causal), int(own_token), 0)
+                 token_positions: bool = False, kernel: int = 0):
+        super().__init__(sinks, window, int(token_positions), int(causal), int(own_token), kernel)
 
 
 class TokenCache(RecsaTree):

@@ -28,6 +28,7 @@ recsa_status check_view(const recsa_view *v) {
   if (v->sinks < 0 || v->window < 0) return fail(RECSA_ERR_INVALID_ARGUMENT, "sinks %d, window %d", v->sinks, v->window);
   if ((int64_t)v->sinks + v->window > ((int64_t)1 << 30))
     return fail(RECSA_ERR_UNSUPPORTED, "sinks %d + window %d > 2^30", v->sinks, v->window);
+  if (v->kernel < 0 || v->kernel > 2) return fail(RECSA_ERR_INVALID_ARGUMENT, "kernel %d (0 .. 2)", v->kernel);
   if (v->sink_positions != 0 && v->sink_positions != 1)
     return fail(RECSA_ERR_INVALID_ARGUMENT, "sink_positions %d (0 or 1)", v->sink_positions);
   return RECSA_OK;
@@ -83,8 +84,14 @@ DenseArgs dense_args(const recsa_params *p, const recsa_tree *t, const recsa_vie
   return a;
 }
 
-// Query rows of a KV group from which the chunk kernel's tiles of 256 rows take over.
-constexpr int64_t kChunkRows = 64;
+// Whether a bf16 output takes the chunk kernel.  With K keys in all (sequences x KV heads x keys
+// seen) and t tiles of 16 query rows a group, the rows kernel measured 18 us + 0.12 ns K t, the
+// chunk kernel (up to 256 rows) 38 us + 0.2 ns K: at 32 heads of 8192 keys they cross at 2 tiles
+// (85 and 89 us), at 8 heads of 8192 between 4 and 6 (48 and 57, 60 and 57 us), at 2 heads of 2000
+// the rows kernel is ahead at 32 (31 and 44 us).
+bool chunk_pays(int64_t keys, int64_t rows) {
+  return (double)keys * (double)(12 * ceil_div(rows, 16) - 20) > 2e6;
+}
 
 // The work items of the launch fit its grid.
 recsa_status check_rows(const DenseArgs &a) {
@@ -101,12 +108,19 @@ int64_t max_keys(const DenseArgs &a) {
   return std::min<int64_t>(n, (int64_t)a.sinks + a.window + (a.causal ? std::min(a.nq, 256 >> a.group_shift) : 0));
 }
 
-recsa_status attend(DenseArgs a, void *out, int32_t out_is_fp32, size_t ws_bytes, void *stream) {
+// The kernel a call asks for, before anything is queued.
+recsa_status check_kernel(const recsa_view *v, int32_t out_is_fp32) {
+  if (v && v->kernel == 2 && out_is_fp32) return fail(RECSA_ERR_UNSUPPORTED, "the chunk kernel writes bf16 outputs");
+  return RECSA_OK;
+}
+
+recsa_status attend(DenseArgs a, const recsa_view *v, void *out, int32_t out_is_fp32, size_t ws_bytes, void *stream) {
   a.out = out;
   a.out_fp32 = out_is_fp32 ? 1 : 0;
+  const int kernel = v ? v->kernel : 0;
   const int64_t rows = (int64_t)a.nq << a.group_shift;  // of a KV group
   int rc = kNoRoom;
-  if (!a.out_fp32 && rows >= kChunkRows)
+  if (!a.out_fp32 && (kernel == 2 || (kernel == 0 && chunk_pays((int64_t)a.batch * a.hkv * max_keys(a), rows))))
     rc = launch_dense_chunk(a, max_keys(a), (int64_t)(ws_bytes - kDenseImages), stream);
   if (rc == kNoRoom) rc = launch_dense_rows(a, max_keys(a), nullptr, stream);
   return rc != 0 ? cuda_fail(rc, "dense attend") : RECSA_OK;
@@ -153,6 +167,7 @@ RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recs
   TreeGeom g;
   recsa_status s = check_cache(params, tree, &g);
   if (s == RECSA_OK) s = check_view(view);
+  if (s == RECSA_OK) s = check_kernel(view, out_is_fp32);
   if (s != RECSA_OK) return s;
   if (num_queries < 1) return fail(RECSA_ERR_INVALID_ARGUMENT, "num_queries %d < 1", num_queries);
   s = check_buffer(q, "q");
@@ -163,7 +178,7 @@ RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recs
                                  view && view->own_token, ws);
   s = check_rows(a);
   if (s != RECSA_OK) return s;
-  return attend(a, out, out_is_fp32, ws_bytes, stream);
+  return attend(a, view, out, out_is_fp32, ws_bytes, stream);
 }
 
 RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, recsa_tree *tree, const recsa_view *view,
@@ -173,6 +188,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
   TreeGeom g;
   recsa_status s = check_cache(params, tree, &g);
   if (s == RECSA_OK) s = check_view(view);
+  if (s == RECSA_OK) s = check_kernel(view, out_is_fp32);
   if (s != RECSA_OK) return s;
   if (chunk < 1) return fail(RECSA_ERR_INVALID_ARGUMENT, "chunk %d < 1", chunk);
   s = check_buffer(k_new, "k_new");
@@ -201,7 +217,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
     rc = launch_advance_lengths(tree->seq_len, tree->batch, chunk, L2, stream);
     if (rc != 0) return cuda_fail(rc, "advance of the sequence lengths");
   }
-  s = attend(a, out, out_is_fp32, ws_bytes, stream);
+  s = attend(a, view, out, out_is_fp32, ws_bytes, stream);
   if (s == RECSA_OK) tree->length = L2;
   return s;
 }
@@ -213,6 +229,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
   TreeGeom g;
   recsa_status s = check_cache(params, tree, &g);
   if (s == RECSA_OK) s = check_view(view);
+  if (s == RECSA_OK) s = check_kernel(view, out_is_fp32);
   if (s != RECSA_OK) return s;
   if (!tree->seq_len)
     return fail(RECSA_ERR_INVALID_ARGUMENT, "a decode step needs per-sequence lengths (tree->seq_len)");
@@ -232,7 +249,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
   if (rc != 0) return cuda_fail(rc, "append");
   rc = launch_advance_lengths(tree->seq_len, tree->batch, 1, cap, stream);
   if (rc != 0) return cuda_fail(rc, "advance of the sequence lengths");
-  return attend(a, out, out_is_fp32, ws_bytes, stream);
+  return attend(a, view, out, out_is_fp32, ws_bytes, stream);
 }
 
 RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, const recsa_tree *tree,

@@ -52,10 +52,9 @@ struct ChunkSmem {
   int gap[4];                               // whether some token of it before the sequence's end was not
   uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
   uint64_t s_full[2][2], p_full[2][2];
-  uint64_t join, joined, drain[2];
+  uint64_t drain[2];
   uint32_t tmem;
   uint32_t stop;                            // a wait ran out: no role waits any more, all run to their ends
-  int last;
   int scan[kChunkThreads / 32];
   int prefix[kMaxShared + 1];               // key tiles before each item, when items are shared
 };
@@ -69,6 +68,7 @@ struct ChunkArgs {
   int shared;       // 1: the key tiles of all items are dealt out evenly to the blocks
   int key_tiles, query_sets;
   uint32_t *redo;
+  int *prefix;
   // rotated rows: keys [heads][key_tiles] and their loaded tokens; queries [items][1 or 2: for the
   // window's tokens, for the sinks][2 row tiles]
   unsigned char *key_images, *query_images;
@@ -132,14 +132,18 @@ struct Segments {
 };
 // Shared: block c of `blocks` holds key tiles [total c / blocks, total (c + 1) / blocks).
 __device__ __forceinline__ int dealt(int total, int blocks, int c) { return (int)((int64_t)total * c / blocks); }
-__device__ __forceinline__ int sharing_blocks(int total) { return min((int)gridDim.x, total); }
+__device__ __forceinline__ int sharing_blocks(int total, int grid) { return min(grid, total); }
+// A block's part of an item it shares: at most its first segment's and its last's are parts.
+__device__ __forceinline__ float *part_of(const DenseArgs &d, int c, bool first) {
+  return ws_part(d.hdr) + ((int64_t)c * 2 + (first ? 0 : 1)) * (kItemRows * kPartRow);
+}
 __device__ __forceinline__ Segments segments_begin(const ChunkArgs &a, const ChunkSmem &sm) {
   Segments s;
   s.j0 = s.j1 = 0;
   s.at = s.end = s.begin = 0;
   s.item = (int)blockIdx.x - (int)gridDim.x;
   if (a.shared) {
-    const int total = sm.prefix[a.items], blocks = sharing_blocks(total);
+    const int total = sm.prefix[a.items], blocks = sharing_blocks(total, gridDim.x);
     if ((int)blockIdx.x >= blocks) return s;
     s.begin = s.at = dealt(total, blocks, blockIdx.x);
     s.end = dealt(total, blocks, blockIdx.x + 1);
@@ -331,8 +335,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       mbar_init(&sm.s_full[u & 1][u >> 1], 1);
       mbar_init(&sm.p_full[u & 1][u >> 1], kSoftWarps / 2);
     }
-    mbar_init(&sm.join, kSoftWarps);
-    mbar_init(&sm.joined, 1);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
     sm.stop = 0;
@@ -368,6 +370,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
+  if (a.shared && blockIdx.x == 0)  // for dense_join_kernel
+    for (int i = tid; i <= a.items; i += kChunkThreads) a.prefix[i] = sm.prefix[i];
   const uint32_t tmem = sm.tmem;
   Segments sg = segments_begin(a, sm);
   Item it;
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t ts = tmem + lanes + t * kTile, to = tmem + lanes + 2 * kTile + t * kTile;
     const int row = t * kTile + trow, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
-    uint32_t n = 0, n_s = 0, n_join = 0;  // key tiles seen; phases of s_full and join
+    uint32_t n = 0, n_s = 0;  // key tiles seen; phases of s_full
     while (segments_next(a, sm, sg, it)) {
       const bool busy = t == 0 || two_tiles(d, it);
       const bool in = (row >> gs) < it.nq;
@@ -461,14 +465,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       // epilogue: the item's output, or this block's part of it: [32 pieces of 16 bytes][row], then
       // (maximum, sum) [row]
       const bool part = sg.j1 - sg.j0 < it.tiles;
-      auto part_of = [&](int c, bool first) {
-        return ws_part(d.hdr) + ((int64_t)c * 2 + (first ? 0 : 1)) * (kItemRows * kPartRow);
-      };
       const int64_t out_row = ((int64_t)it.b * d.nq + it.q0 + (row >> gs)) * hq + it.h * G + (row & (G - 1));
       uint4 *const po = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(d.out) + out_row * kD);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       bool odd = !(l < INFINITY);
-      float *const mypart = part_of(blockIdx.x, sg.at - (sg.j1 - sg.j0) == sg.begin);
+      float *const mypart = part_of(d, blockIdx.x, sg.at - (sg.j1 - sg.j0) == sg.begin);
 #pragma unroll 1
       for (int g = 0; busy && g < 4; ++g) {
         uint32_t o[32];
@@ -496,77 +497,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
       umma::fence_before_sync();
       if (part) {
         if (busy) reinterpret_cast<float2 *>(mypart + kItemRows * kD)[row] = make_float2(m, l);
-        odd = false;
-        // the item's key tiles are spread over blocks c0 .. c1: the last to arrive joins them in order
-        const int total = sm.prefix[a.items], blocks = sharing_blocks(total);
-        const int w0 = sm.prefix[sg.item], w1 = w0 + it.tiles;
-        auto holder = [&](int w) {  // the block that holds key tile w
-          int c = (int)((int64_t)w * blocks / total);
-          while (dealt(total, blocks, c + 1) <= w) ++c;
-          while (dealt(total, blocks, c) > w) --c;
-          return c;
-        };
-        const int c0 = holder(w0), c1 = holder(w1 - 1);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.join);
-        wait(sm, a, &sm.join, n_join & 1);
-        if (tid == 0) {
-          const int done = atomicAdd(ws_count(d.hdr) + sg.item, 1);
-          sm.last = done == c1 - c0;
-          if (sm.last) ws_count(d.hdr)[sg.item] = 0;  // for the next call
-          __threadfence();
-          mbar_arrive(&sm.joined);
-        }
-        wait(sm, a, &sm.joined, n_join & 1);
-        ++n_join;
-        __threadfence();
-        if (sm.last && busy) {
-          // the item is in block c's first segment if the block begins inside it
-          auto from = [&](int c) { return part_of(c, dealt(total, blocks, c) >= w0); };
-          auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(from(c) + kItemRows * kD) + row); };
-          float mm = -INFINITY, ll = 0.f;
-          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, stats(c).x);
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = stats(c);
-            if (ml.x != -INFINITY) ll += ml.y * exp2_approx(ml.x - mm);
-          }
-          const float iv = ll == 0.f ? 0.f : 1.f / ll;
-          odd = !(ll < INFINITY);
-          auto factor = [&](float mc) { return mc == -INFINITY ? 0.f : exp2_approx(mc - mm) * iv; };
-#pragma unroll 1
-          for (int g = 0; g < 4; ++g) {  // 32 dimensions, two parts in flight
-            float acc[32] = {};
-#pragma unroll 1
-            for (int c = c0; c <= c1; c += 2) {
-              const bool two = c < c1;
-              const float *pa = from(c), *pb = two ? from(c + 1) : pa;
-              const float4 *sa = reinterpret_cast<const float4 *>(pa) + g * 8 * kItemRows + row;
-              const float4 *sb = reinterpret_cast<const float4 *>(pb) + g * 8 * kItemRows + row;
-              const float ma = stats(c).x, mb = two ? stats(c + 1).x : -INFINITY;
-              float4 u[8], v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) u[i] = __ldcg(sa + i * kItemRows);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = two ? __ldcg(sb + i * kItemRows) : make_float4(0.f, 0.f, 0.f, 0.f);
-              const float fa = factor(ma), fb = factor(mb);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                acc[4 * i] += fa * u[i].x + fb * v[i].x, acc[4 * i + 1] += fa * u[i].y + fb * v[i].y;
-                acc[4 * i + 2] += fa * u[i].z + fb * v[i].z, acc[4 * i + 3] += fa * u[i].w + fb * v[i].w;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) odd |= !(fabsf(acc[i]) < INFINITY);
-            if (in) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                po[g * 4 + i] = make_uint4(cvt_bf16x2(acc[8 * i], acc[8 * i + 1]), cvt_bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
-                                           cvt_bf16x2(acc[8 * i + 4], acc[8 * i + 5]),
-                                           cvt_bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
-            }
-          }
-        }
+        odd = false;  // dense_join_kernel joins the parts
       }
       if (odd && in) mark_again(a, it.b, it.h, it.q0 / (kItemRows >> gs));
     }
@@ -707,6 +638,60 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
   if (warp == 12) umma::tmem_dealloc(tmem, 512);
 }
 
+// Joins the parts of the items that several blocks of the chunk kernel shared, in the blocks' order:
+// 32 rows of an item a block, a warp's lanes along the rows.  (Joined by the last of the sharing
+// blocks instead, 18 parts took that block 28 us.)
+__global__ void __launch_bounds__(256) dense_join_kernel(ChunkArgs a, int chunk_blocks) {
+  const DenseArgs &d = a.d;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;
+  constexpr int kBlocks = kItemRows / 32;
+  const int item = blockIdx.x / kBlocks, row = blockIdx.x % kBlocks * 32 + (threadIdx.x & 31), piece0 = threadIdx.x >> 5;
+  const int total = __ldg(a.prefix + a.items), blocks = sharing_blocks(total, chunk_blocks);
+  const int w0 = __ldg(a.prefix + item), w1 = __ldg(a.prefix + item + 1);
+  auto holder = [&](int w) {  // the block that holds key tile w
+    int c = (int)((int64_t)w * blocks / total);
+    while (dealt(total, blocks, c + 1) <= w) ++c;
+    while (dealt(total, blocks, c) > w) --c;
+    return c;
+  };
+  const int c0 = holder(w0), c1 = holder(w1 - 1);
+  if (c0 == c1) return;
+  const Item it = chunk_item(a, item);
+  const int gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
+  if ((row >> gs) >= it.nq) return;
+  // the item is in block c's first segment if the block begins inside it
+  auto from = [&](int c) { return part_of(d, c, dealt(total, blocks, c) >= w0); };
+  auto stats = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(from(c) + kItemRows * kD) + row); };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, stats(c).x);
+  float4 acc[4] = {};
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 ml = stats(c);
+    const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
+    const float4 *src = reinterpret_cast<const float4 *>(from(c)) + row;
+    l += f * ml.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 u = __ldcg(src + (piece0 + 8 * i) * kItemRows);
+      acc[i].x += f * u.x, acc[i].y += f * u.y, acc[i].z += f * u.z, acc[i].w += f * u.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  bool odd = !(l < INFINITY);
+  uint16_t *const out = reinterpret_cast<uint16_t *>(d.out) +
+                        (((int64_t)it.b * d.nq + it.q0 + (row >> gs)) * hq + it.h * G + (row & (G - 1))) * kD;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x[4] = {acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) odd |= !(fabsf(x[k]) < INFINITY);
+    *reinterpret_cast<uint2 *>(out + (piece0 + 8 * i) * 4) = make_uint2(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]));
+  }
+  if (odd) mark_again(a, it.b, it.h, it.q0 / (kItemRows >> gs));
+}
+
 // The most key tiles a head's queries see.
 int64_t most_key_tiles(const DenseArgs &d) {
   const int64_t all = ceil_div(std::max(d.length, 1), kTile);
@@ -724,6 +709,7 @@ int launch_dense_chunk(const DenseArgs &d, int64_t max_keys, int64_t image_bytes
   const int64_t chunk_tiles = ceil_div(d.nq, per), heads = (int64_t)d.batch * d.hkv;
   a.d.tiles = (int)chunk_tiles;
   a.redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(d.hdr) + kDenseRedo);
+  a.prefix = reinterpret_cast<int *>(reinterpret_cast<char *>(d.hdr) + kDensePrefix);
   a.key_tiles = (int)most_key_tiles(d);
   a.query_sets = d.window && d.sinks && d.rank_sinks ? 2 : 1;
   const int sms = std::min(dense_sm_count(), kMaxChunkBlocks);
@@ -756,7 +742,9 @@ int launch_dense_chunk(const DenseArgs &d, int64_t max_keys, int64_t image_bytes
       e = cudaGetLastError();
       if (e != cudaSuccess) return (int)e;
       const int64_t work = a.shared ? a.items * tiles : a.items;
-      dense_chunk_kernel<<<(unsigned)std::min<int64_t>(work, sms), kChunkThreads, kChunkSmem, (cudaStream_t)stream>>>(a);
+      const int blocks = (int)std::min<int64_t>(work, sms);
+      dense_chunk_kernel<<<(unsigned)blocks, kChunkThreads, kChunkSmem, (cudaStream_t)stream>>>(a);
+      if (a.shared) dense_join_kernel<<<(unsigned)(a.items * (kItemRows / 32)), 256, 0, (cudaStream_t)stream>>>(a, blocks);
       e = cudaGetLastError();
       if (e != cudaSuccess) return (int)e;
     }

@@ -17,7 +17,8 @@ constexpr size_t kDenseFreq = kWsHeader;                                   // ui
 constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float4[64][32] (cos, cos', sin, sin')
 constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
 constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t) + 256;  // marks of items to compute again
-constexpr size_t kDensePart = kDenseRedo + kMaxShared * sizeof(uint32_t);  // partial results
+constexpr size_t kDensePrefix = kDenseRedo + kMaxShared * sizeof(uint32_t);  // key tiles before each item of a chunk
+constexpr size_t kDensePart = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
 constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call

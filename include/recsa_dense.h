@@ -41,6 +41,10 @@ extern "C" {
  *                    last n tokens of the cache: query i sits at p = L - n + i.
  *   own_token      : with causal: 1 = a query also sees its own token (p = L - n + i + 1).
  *                    0 is the position convention of recsa_prefill_chunk.
+ *   kernel         : launch-shape override of the attention calls: 0 = automatic by the sizes;
+ *                    1 = the rows kernel (8 or 16 query rows a block; every output type);
+ *                    2 = the chunk kernel (256 query rows a block on tcgen05; bf16 outputs,
+ *                    else RECSA_ERR_UNSUPPORTED).  Results agree up to their rounding.
  * A query whose p is 0 or less (a sequence shorter than the chunk) sees nothing. */
 typedef struct recsa_view {
   int32_t sinks;
@@ -48,7 +52,7 @@ typedef struct recsa_view {
   int32_t sink_positions;
   int32_t causal;
   int32_t own_token;
-  int32_t reserved;
+  int32_t kernel;
 } recsa_view;
 
 /* Bytes of the workspace of the dense calls on caches of `batch` sequences of up to
@@ -70,8 +74,9 @@ RECSA_API recsa_status recsa_dense_workspace_init(const recsa_params *params, in
  *   q   : bf16 [batch][num_queries][Hq][128], pre-RoPE.
  *   out : [batch][num_queries][Hq][128], fp32 if out_is_fp32 else bf16.
  * With an fp32 output scores and probabilities keep 16 bits of each operand on the tensor
- * cores (the output is within about 1e-5 of the formula, relative); with a bf16 output the
- * rotated rows and the probabilities are rounded to bf16 first, as the output is. */
+ * cores (the output is within about 1e-5 of the formula, relative).  With a bf16 output the
+ * chunk kernel rounds the rotated rows to fp16 and the probabilities to bf16 (the output is
+ * within about 2.5e-3, its own rounding 1.7e-3 of that). */
 RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recsa_tree *tree, const recsa_view *view,
                                           const void *q, int32_t num_queries, void *out, int32_t out_is_fp32,
                                           void *ws, size_t ws_bytes, recsa_stream_t stream);

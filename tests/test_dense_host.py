@@ -83,6 +83,10 @@ def test_bad_views(op):
     refused(INVALID, *call(op, t=t, view=R.View(sinks=-1, window=4)))
     refused(INVALID, *call(op, t=t, view=R.View(window=-1)))
     refused(UNSUPPORTED, *call(op, t=t, view=R.View(sinks=1 << 30, window=1)))
+    refused(INVALID, *call(op, t=t, view=R.View(kernel=3)))
+    refused(INVALID, *call(op, t=t, view=R.View(kernel=-1)))
+    if op != "weights":
+        refused(UNSUPPORTED, *call(op, t=t, view=R.View(kernel=R.DENSE_CHUNK)))  # (the calls here write fp32)
     v = R.View(window=4)
     v.sink_positions = 2
     refused(INVALID, *call(op, t=t, view=v))

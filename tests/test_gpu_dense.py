@@ -1,18 +1,19 @@
 """The dense cache operators on a B200 against their definitions in 64 bits.
 
 Tolerances.  A score is c <q', k'> of rotated rows, |q'| = |q|, |k'| = |k|; A = c max|q| max|k|
-bounds every |score| (Cauchy).
- * fp32 output: each operand of a product is kept as two bf16 parts (off by at most 2^-18 of
-   it) and the product of the two small parts is dropped (2^-18): 3 * 2^-18 A, and with the fp32
-   rotation and sums under 2^-16 A a score.  A weight e^s / sum e^s then moves by at most twice
-   that, relative, and a probability's own two parts add 2^-18: |out - exact| <=
-   (2 * 2^-16 A + 2^-16) max|v|.  The errors of the 128 terms and of the tokens are independent,
-   so the 2-norm of all errors stays under 2^-16 of the output's.
- * bf16 output: one bf16 rounding (half a step, 2^-9, 2^-9/sqrt 3 rms) of each rotated q and k
-   element, of each probability and of the output.  Scores of spread sigma <= 2 are then
-   sqrt(2) 2^-9/sqrt(3) sigma off (rms), 3.2e-3; with the other two (1.1e-3 each) 3.6e-3 of the
-   output's norm, and 2^-7 is allowed.
- * weights (fp32): each is a sum of softmax weights of fp32-output accuracy:
+bounds every |score| (Cauchy).  bf16 rounds by at most 2^-8 of a value (half a step), 2^-8/sqrt 3 of
+its power of two rms; what a first rounding leaves is rounded again, so two parts are off by 2^-16.
+ * fp32 output and the rows kernel: a score's operands are two parts each and the product of the
+   two small parts is dropped: three errors of at most 2^-16 of |q' k'|, of independent sign over the
+   128 terms, so that a score is off by 2^-16 A with ease (the bound 3 * 2^-16 A would need all of
+   them to agree).  A weight e^s / sum e^s moves by at most twice that, relative, and a probability's
+   own two parts add 2^-16: |out - exact| <= (2 * 2^-16 A + 2^-16) max|v|.  Over an output's tokens
+   the errors are independent as well: their 2-norm stays under 2^-16 of the output's.
+ * bf16 output: one rounding of the output and, in the chunk kernel, one of each probability: both
+   are 2^-8/sqrt 3 rms of a value's power of two, 1.7e-3 of the value's norm; rotated rows in fp16
+   (half a step 2^-11) add 2^-11 sigma to a score of spread sigma <= 2.  Together 2.6e-3; 2^-7 is
+   allowed.
+ * weights (fp32): each is a sum of softmax weights of two-part scores:
    |w - exact| <= (2 * 2^-16 A + 2^-16) w, and 2^-16 in the norm as above.
 """
 
@@ -128,19 +129,21 @@ def split_view(view):
     return v, dict(causal=causal, own=own, **ref)
 
 
-@pytest.mark.parametrize("fp32", [True, False])
 @pytest.mark.parametrize("shape", SHAPES, ids=[f"{i}" for i in range(len(SHAPES))])
-def test_attend(shape, fp32):
+def test_attend(shape):
     B, H, G, L, n, page, lens, view = shape
     c = Case(B, H, G, L, n, seed=L * 31 + n, page=page, lens=lens, spare=5)
     v, ref = split_view(view)
-    check(c.attend(fp32, v), c.want(**ref), fp32, c.bound())
+    want = c.want(**ref)
+    for fp32, kernel in ((True, R.DENSE_AUTO), (False, R.DENSE_AUTO), (False, R.DENSE_ROWS), (False, R.DENSE_CHUNK)):
+        v.kernel = kernel
+        check(c.attend(fp32, v), want, fp32, c.bound())
 
 
 def test_same_call_gives_the_same_bits():
     c = Case(2, 2, 4, 3000, 3, seed=5)
-    for fp32 in (True, False):
-        v = R.View(causal=True, own_token=True)
+    for fp32, kernel in ((True, R.DENSE_ROWS), (False, R.DENSE_ROWS), (False, R.DENSE_CHUNK)):
+        v = R.View(causal=True, own_token=True, kernel=kernel)
         first = c.attend(fp32, v)
         for _ in range(3):
             assert torch.equal(first, c.attend(fp32, v))
@@ -157,20 +160,26 @@ def test_hidden_tokens_do_not_reach_a_query(view, bad, n):
     L = 400
     c = Case(1, 2, 4, L, n, seed=11)
     v, ref = split_view(view)
-    plain = {fp32: c.attend(fp32, v) for fp32 in (True, False)}
+    runs = ((True, R.DENSE_ROWS), (False, R.DENSE_ROWS), (False, R.DENSE_CHUNK))
+
+    def attend(fp32, kernel):
+        v.kernel = kernel
+        return c.attend(fp32, v)
+
+    plain = {r: attend(*r) for r in runs}
+    want = c.want(**ref)
     hit = L - n // 2  # a token in the middle of the chunk
     old = L - n - 10  # one before it, that a window leaves behind part way through the chunk
     spots = [hit] + ([old] if "window" in view else [])
     for t in spots:
         c.cache.k_tok[0, :, t] = bad
         c.cache.v_tok[0, :, t] = bad
-    want = c.want(**ref)
-    for fp32 in (True, False):
-        got = c.attend(fp32, v)
-        blind = [i for i, p in enumerate(F.positions(L, n, True, True))
-                 if not any(t < p and ("window" not in view or t >= p - 20) for t in spots)]
-        if fp32 or n == 6:
-            assert torch.equal(got[0, blind], plain[fp32][0, blind])
+    blind = [i for i, p in enumerate(F.positions(L, n, True, True))
+             if not any(t < p and ("window" not in view or t >= p - 20) for t in spots)]
+    for r in runs:
+        got = attend(*r)
+        if r[1] == R.DENSE_ROWS:
+            assert torch.equal(got[0, blind], plain[r][0, blind])
         else:
             check(got[:, blind], want[:, blind], False, 0.0)
         if bad != bad:
@@ -181,9 +190,9 @@ def test_a_hidden_value_is_ignored_even_where_its_weight_would_be_zero():
     """Infinite values alone (finite keys): a masked key's weight is zero, and zero times infinity
     must not appear."""
     L, n = 300, 140
-    for G, fp32 in ((1, True), (4, False), (8, False)):
+    for G, fp32, kernel in ((1, True, R.DENSE_ROWS), (4, False, R.DENSE_CHUNK), (8, False, R.DENSE_CHUNK)):
         c = Case(1, 1, G, L, n, seed=12)
-        v = R.View(causal=True, own_token=True)
+        v = R.View(causal=True, own_token=True, kernel=kernel)
         plain = c.attend(fp32, v)
         c.cache.v_tok[0, :, L - 3] = float("inf")
         got = c.attend(fp32, v)
@@ -400,6 +409,7 @@ def test_chunks(case):
     c = Case(case["B"], case["H"], case["G"], case["L"], case["n"], seed=case["L"] + case["n"], page=case.get("page", 0),
              lens=lens, spare=3)
     v, ref = split_view(case["view"])
+    v.kernel = R.DENSE_CHUNK
     got = c.attend(False, v)
     check(got, c.want(**ref), False, 0.0)
     for _ in range(2):
@@ -418,7 +428,7 @@ def test_chunk_rows_beyond_half_precision():
         else:
             c.k[:, :, 100:140] *= 2.0 ** 17
             c.cache.k_tok.copy_(c.k)
-        got = c.attend(False, R.View(causal=True, own_token=True))
+        got = c.attend(False, R.View(causal=True, own_token=True, kernel=R.DENSE_CHUNK))
         check(got, c.want(causal=True, own=True, scale=c.softmax), False, 0.0)
 
 
