@@ -14,20 +14,25 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;                  // keys of a step
 constexpr int kStepBytes = kStep * kRowBytes;
-constexpr int kTableStride = kHalf * 8 + 64;  // bytes of a table row in shared memory
+constexpr int kTableStride = kHalf * 8;       // bytes of a table row in shared memory
 constexpr int kQStride = kD + 4;              // floats of a query row in shared memory
 constexpr int kOStride = kD + 8;              // floats of an output row in shared memory
+constexpr int kDealtSequences = kThreads;     // sequences whose steps can be dealt out (a thread counts one's)
+constexpr int kDealtSteps = 16;               // steps a block is worth starting for
 constexpr float kRowsRescale = 64.f;          // a row's maximum may lag by 2^64 before its output is rescaled
 
 template <int R>  // query rows of a tile: queries x heads of a KV group
 struct RowsSmem {
   unsigned char stage[kWarps][2][kStepBytes];  // [K, V]
-  unsigned char table[kSpan * kTableStride];   // two frequencies: cos, cos', sin, sin'
+  // two frequencies: cos, cos', sin, sin'; the pieces of odd rows are moved by four places, so that
+  // the two rows a quarter warp reads lie in different banks
+  unsigned char table[kSpan * kTableStride];
   float q[2][R][kQStride];             // [window, sinks], scaled, turned to the tile's base position
   float4 ang[kWarps][kHalf / 2];       // a warp's rotation of the query rows, as the table
   float m[kWarps][R], l[kWarps][R];
   int pos[R];                          // a row's position; 0 or less: nothing visible
   int last;
+  int dealt[kDealtSequences + 1];      // steps before each sequence, when steps are dealt out to the blocks
 };
 
 // One step's rows: 16 keys from token T, those outside [lo, hi) or on a page outside the pool as
@@ -106,7 +111,8 @@ __device__ __forceinline__ void load_table(const DenseArgs &a, unsigned char *ta
 #pragma unroll
   for (int i = 0; i < kSpan * kHalf / 2 / kThreads; ++i) {
     const int e = tid + i * kThreads;
-    cp_async16(dst + (e / (kHalf / 2)) * kTableStride + (e % (kHalf / 2)) * 16, ws_table(a.hdr) + 2 * e, true);
+    const int r = e / (kHalf / 2), piece = e % (kHalf / 2);
+    cp_async16(dst + r * kTableStride + ((piece ^ ((r & 1) << 2)) << 4), ws_table(a.hdr) + 2 * e, true);
   }
 }
 
@@ -149,6 +155,7 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
   const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: lanes 0-15 the first 8 dimensions' rows, 16-31 the next 8
   const uint32_t lbase = sk + lrow * kRowBytes;
   const unsigned char *tr = table + ((T & (kSpan - 1)) + (lane >> 2)) * kTableStride + (lane & 3) * 16;
+  const int odd = ((lane >> 2) & 1) << 6;  // 4 pieces (T is even)
   float lo[NR][4];
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
@@ -158,7 +165,7 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
     uint32_t uh[4], ul[4], vh[4], vl[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (2 * ks + (i >> 1)) * 64);
+      const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (((2 * ks + (i >> 1)) * 64) ^ odd));
       const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]), minus = f2(-1.f, -1.f);
       const F2 U = f2_fma(f2_mul(Y, sn), minus, f2_mul(X, cs)), V = f2_fma(X, sn, f2_mul(Y, cs));
       const float2 u = f2_get(U), v = f2_get(V);
@@ -223,6 +230,19 @@ __device__ __forceinline__ Range tile_range(const DenseArgs &a, int p_min, int p
   return r;
 }
 
+// `total` steps dealt out evenly to as many of the grid's blocks as are worth starting.
+struct Dealt {
+  int total, blocks;
+  __device__ __forceinline__ explicit Dealt(int t) : total(t), blocks(min((int)gridDim.x, max(1, t / kDealtSteps))) {}
+  __device__ __forceinline__ int begin(int block) const { return (int)((int64_t)total * block / blocks); }
+  __device__ __forceinline__ int holder(int step) const {  // the block that holds a step
+    int block = (int)((int64_t)step * blocks / total);
+    while (begin(block + 1) <= step) ++block;
+    while (begin(block) > step) --block;
+    return block;
+  }
+};
+
 // One tile of 8 NR query rows (queries x heads of a KV group) against one block's share of the keys
 // they see.  Each warp walks its own steps of 16 keys with an online softmax, its keys and values
 // fetched one step ahead with cp.async into memory of its own, so warps never wait for one another
@@ -233,7 +253,7 @@ __device__ __forceinline__ Range tile_range(const DenseArgs &a, int p_min, int p
 // slots of the ~88 its SM has meanwhile.
 // MODE 0: the output.  MODE 1: the rows' log2-sum-exp to `lse`.  MODE 2: the output of the tiles
 // that the chunk kernel marked in `redo`, if any.
-template <int NR, int MODE>
+template <int NR, int MODE, bool DEAL>
 __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     dense_rows_kernel(DenseArgs a, int items, float *lse, uint32_t *redo, int chunk_tiles) {
   constexpr int R = 8 * NR;
@@ -254,27 +274,84 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   const int r = lane >> 2, c = lane & 3;
   const uint32_t sk = smem_u32(sm.stage[warp][0]), sv = sk + kStepBytes;
 
-  for (int work = blockIdx.x; work < items * a.nsplit; work += gridDim.x) {
-  const int item = work / a.nsplit, split = work % a.nsplit;
-  const int tile = item % a.tiles, bh = a.bh0 + item / a.tiles;
-  const int b = bh / a.hkv, h = bh % a.hkv;
+  // Sequences of unequal length: their steps (a head's one after the other) are dealt out evenly
+  // to the blocks instead of an equal number of blocks a head.
+  int at = 0, end = 0;
+  if (DEAL) {
+    int steps = 0;
+    if (tid < a.batch) {
+      const int len = dense_length(a, tid, blockIdx.x == 0);
+      steps = max(1, tile_range(a, dense_position(a, len, 0), dense_position(a, len, a.nq - 1)).total);
+    }
+    int incl = steps * a.hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int *const warp_sum = reinterpret_cast<int *>(sm.ang);  // (free until the first turn)
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    sm.dealt[tid + 1] = incl;
+    if (tid == 0) sm.dealt[0] = 0;
+    __syncthreads();
+    const Dealt d(sm.dealt[a.batch]);
+    if ((int)blockIdx.x >= d.blocks) return;
+    at = d.begin(blockIdx.x);
+    end = d.begin(blockIdx.x + 1);
+  }
+
+  bool table = false;
+  for (int work = blockIdx.x; DEAL ? at < end : work < items * a.nsplit; work += gridDim.x) {
+  int item, split = 0, tile, bh, b, h;
+  if (DEAL) {
+    int lo = 0, hi = a.batch - 1;  // the sequence that holds step `at`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (sm.dealt[mid] <= at) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    h = (at - sm.dealt[b]) / ((sm.dealt[b + 1] - sm.dealt[b]) / a.hkv);
+    item = bh = b * a.hkv + h;
+    tile = 0;
+  } else {
+    item = work / a.nsplit;
+    split = work % a.nsplit;
+    tile = item % a.tiles;
+    bh = a.bh0 + item / a.tiles;
+    b = bh / a.hkv;
+    h = bh % a.hkv;
+  }
   const int q0 = tile * (R >> gs), nq = min(R >> gs, a.nq - q0);  // the tile's queries
   if (MODE == 2 && !redo[redo_slot(bh, chunk_tiles, q0 / (256 >> gs))]) continue;
-  const int len = dense_length(a, b, tid == 0 && tile == 0 && split == 0 && h == 0);
+  const int len = dense_length(a, b, !DEAL && tid == 0 && tile == 0 && split == 0 && h == 0);
   const int p_min = dense_position(a, len, q0), p_max = dense_position(a, len, q0 + nq - 1);
   const Range rg = tile_range(a, p_min, p_max);
   const int base_sink = sink_position(a, p_max);
 
+  int begin, stop;  // the block's steps of the tile
+  if (DEAL) {
+    const int steps = (sm.dealt[b + 1] - sm.dealt[b]) / a.hkv;
+    begin = at - (sm.dealt[b] + h * steps);
+    stop = min(steps, begin + end - at);
+    at += stop - begin;
+    stop = min(stop, rg.total);  // (a tile without keys counts as one step)
+  } else {
+    begin = (int)((int64_t)rg.total * split / a.nsplit);
+    stop = (int)((int64_t)rg.total * (split + 1) / a.nsplit);
+  }
   // this warp's steps; the first loads are on their way while the query rows are turned
-  const int64_t parts = (int64_t)a.nsplit * kWarps, part = (int64_t)split * kWarps + warp;
-  const int st0 = (int)(rg.total * part / parts), st1 = (int)(rg.total * (part + 1) / parts);
+  const int st0 = begin + (int)((int64_t)(stop - begin) * warp / kWarps),
+            st1 = begin + (int)((int64_t)(stop - begin) * (warp + 1) / kWarps);
   auto place = [&](int st) {
     const bool sink = rg.sink(st);
     return place_step(a, b, h, rg.token(st), sink ? 0 : rg.lo2, sink ? rg.hi1 : rg.hi2, lane);
   };
   // MODE 1 has no values: its keys alternate between the two halves of the stage
   Step cur = {0, 0u}, next = {0, 0u};
-  if (work == blockIdx.x) load_table(a, sm.table, tid);  // with the first step's keys
+  if (!table) load_table(a, sm.table, tid);  // with the first step's keys
+  table = true;
   if (st0 < st1) {
     cur = place(st0);
     load_step(a, a.k, cur, PV || !(st0 & 1) ? sk : sv, lane);
@@ -551,8 +628,23 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     }
   }
   bool write = true;
-  if (a.nsplit > 1) {  // leave this block's part; the last block of the tile joins them in order
-    float *part_row = ws_part(a.hdr) + ((int64_t)work * R + row) * kPartRow;
+  // the blocks that share the tile, and where the part of the j-th of them is
+  int sharing = a.nsplit, first_block = 0, item_at = 0;
+  const Dealt dealt(DEAL ? sm.dealt[a.batch] : 1);
+  if (DEAL) {
+    const int steps = (sm.dealt[b + 1] - sm.dealt[b]) / a.hkv;
+    item_at = sm.dealt[b] + h * steps;
+    first_block = dealt.holder(item_at);
+    sharing = dealt.holder(item_at + steps - 1) - first_block + 1;
+  }
+  auto part_at = [&](int j) {  // dealt out: in a block's first segment or its last
+    const int64_t slot = DEAL ? (int64_t)(first_block + j) * 2 + (dealt.begin(first_block + j) >= item_at ? 0 : 1)
+                              : (int64_t)item * a.nsplit + j;
+    return ws_part(a.hdr) + slot * (R * kPartRow);
+  };
+  if (sharing > 1) {  // leave this block's part; the last block of the tile joins them in order
+    float *part_row =
+        part_at(DEAL ? (int)blockIdx.x - first_block : split) + row * kPartRow;
     if (d0 == 0) *reinterpret_cast<float2 *>(part_row) = make_float2(mx, sum);
     if (PV) {
 #pragma unroll
@@ -563,29 +655,28 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     __syncthreads();
     if (tid == 0) {
       const int done = atomicAdd(ws_count(a.hdr) + item, 1);
-      sm.last = done == a.nsplit - 1;
+      sm.last = done == sharing - 1;
       if (sm.last) ws_count(a.hdr)[item] = 0;  // for the next call
     }
     __syncthreads();
     write = sm.last;
     if (write) {
       __threadfence();
-      const float *p0 = ws_part(a.hdr) + ((int64_t)item * a.nsplit * R + row) * kPartRow;
-      const int64_t stride = (int64_t)R * kPartRow;
       mx = -INFINITY;
       sum = 0.f;
 #pragma unroll 4
-      for (int j = 0; j < a.nsplit; ++j) mx = fmaxf(mx, __ldcg(p0 + j * stride));
+      for (int j = 0; j < sharing; ++j) mx = fmaxf(mx, __ldcg(part_at(j) + row * kPartRow));
 #pragma unroll
       for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
 #pragma unroll 8
-      for (int j = 0; j < a.nsplit; ++j) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p0 + j * stride));
+      for (int j = 0; j < sharing; ++j) {
+        const float *p = part_at(j) + row * kPartRow;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p));
         const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mx);
         float4 u[kPer / 4];
         if (PV) {
 #pragma unroll
-          for (int i = 0; i < kPer / 4; ++i) u[i] = __ldcg(reinterpret_cast<const float4 *>(p0 + j * stride + 4 + d0) + i);
+          for (int i = 0; i < kPer / 4; ++i) u[i] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + d0) + i);
         }
         if (ml.x == -INFINITY) continue;
         sum += f * ml.y;
@@ -695,11 +786,11 @@ int opt_in(K kernel, size_t bytes) {
 // Blocks of the rows kernel an SM holds.
 constexpr int blocks_per_sm(int nr) { return nr == 1 ? 2 : 1; }
 
-template <int NR, int MODE>
+template <int NR, int MODE, bool DEAL = false>
 int run_rows(const DenseArgs &a, int64_t items, int64_t grid, float *lse, uint32_t *redo, int chunk_tiles, void *stream) {
-  const int rc = opt_in(dense_rows_kernel<NR, MODE>, sizeof(RowsSmem<8 * NR>));
+  const int rc = opt_in(dense_rows_kernel<NR, MODE, DEAL>, sizeof(RowsSmem<8 * NR>));
   if (rc) return rc;
-  dense_rows_kernel<NR, MODE><<<(unsigned)grid, kThreads, sizeof(RowsSmem<8 * NR>), (cudaStream_t)stream>>>(
+  dense_rows_kernel<NR, MODE, DEAL><<<(unsigned)grid, kThreads, sizeof(RowsSmem<8 * NR>), (cudaStream_t)stream>>>(
       a, (int)items, lse, redo, chunk_tiles);
   return (int)cudaGetLastError();
 }
@@ -747,8 +838,20 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
   const int nr = ((int64_t)a.nq << a.group_shift) <= 8 ? 1 : 2;
   const int per = (8 * nr) >> a.group_shift;
   a.tiles = (a.nq + per - 1) / per;
-  const int64_t items = (a.heads ? a.heads : (int64_t)a.batch * a.hkv) * a.tiles;
-  a.nsplit = pick_split(items, max_keys, dense_sm_count() * blocks_per_sm(nr), 8 * nr);
+  const int64_t all = (int64_t)a.batch * a.hkv, items = (a.heads ? a.heads : all) * a.tiles;
+  const int places = dense_sm_count() * blocks_per_sm(nr);
+  // Per-sequence lengths: what the host knows is their bound, so the steps are dealt out on the device.
+  // That costs a block its start and a second segment, so not where blocks have few steps anyway
+  // (24 x 4 heads of up to 19001 tokens: 139 -> 125 us; 6 x 2 of 780: 20 -> 30 us).
+  const int64_t steps = all * (ceil_div(max_keys, kStep) + 2);
+  if (a.seq_len && steps >= 64 * (int64_t)places && steps < (int64_t)1 << 31 && a.tiles == 1 && a.batch <= kDealtSequences && items == all && items <= kMaxShared) {
+    a.nsplit = 1;
+    if (lse) return nr == 1 ? run_rows<1, 1, true>(a, items, places, lse, nullptr, 0, stream)
+                            : run_rows<2, 1, true>(a, items, places, lse, nullptr, 0, stream);
+    return nr == 1 ? run_rows<1, 0, true>(a, items, places, nullptr, nullptr, 0, stream)
+                   : run_rows<2, 0, true>(a, items, places, nullptr, nullptr, 0, stream);
+  }
+  a.nsplit = pick_split(items, max_keys, places, 8 * nr);
   const int64_t grid = items * a.nsplit;
   if (lse)
     return nr == 1 ? run_rows<1, 1>(a, items, grid, lse, nullptr, 0, stream)

@@ -368,6 +368,23 @@ def test_another_stream_and_two_workspaces():
         assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("B,H,G,L,n,page,lens,view", [
+    (5, 8, 4, 9000, 1, 16, [9000, 17, 0, 4000, 8999], {}),  # long enough for the steps to be dealt out
+    (3, 16, 2, 9000, 4, 0, [300, 9000, 2], dict(causal=True, own=True)),
+    (40, 8, 8, 1200, 1, 64, [1200 - 29 * i for i in range(40)], {}),
+    (5, 8, 4, 9000, 1, 0, [9000, 17, 0, 4000, 8999], dict(sinks=20, window=6000)),
+])
+def test_uneven_sequences(B, H, G, L, n, page, lens, view):
+    c = Case(B, H, G, L, n, seed=L + B, page=page, lens=lens, spare=5)
+    v, ref = split_view(view)
+    check(c.attend(True, v), c.want(**ref), True, c.bound())
+    if not view.get("window"):
+        got = torch.zeros(B, H, c.cap, device="cuda")
+        R.accumulate_weights(c.p, c.cache, c.qd, got, c.ws, v, accumulate=False)
+        want = c.want(want_weights=True, **ref)
+        assert float((got.double().cpu() - want).norm() / want.norm()) <= 2.0 ** -16
+
+
 def test_far_rows_and_far_positions():
     """Rows past 2^31 elements of the cache; positions where an fp32 angle would be worthless."""
     H, G, cap, L = 8, 4, 1 << 20, (1 << 20) - 3
