@@ -268,14 +268,13 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
   if (s != RECSA_OK) return s;
   const DenseArgs a = dense_args(params, tree, view, q, num_queries, tree->length, view && view->causal,
                                  view && view->own_token, ws);
-  const int64_t rows = ((int64_t)num_queries << a.group_shift) * a.hkv * a.batch;
-  if (rows > kMaxDenseLse) return fail(RECSA_ERR_UNSUPPORTED, "%lld query rows > %lld", (long long)rows,
-                                       (long long)kMaxDenseLse);
+  s = check_rows(a);
+  if (s != RECSA_OK) return s;
   float *lse = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kDenseLse);
   const int rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, (int64_t)(ws_bytes - kDenseImages), stream);
   if (rc == kNoRoom)
-    return fail(RECSA_ERR_UNSUPPORTED, "the rotated rows of a sequence of %lld tokens and %d queries do not fit a workspace",
-                (long long)tree->length, num_queries);
+    return fail(RECSA_ERR_UNSUPPORTED, "the rotated keys of a sequence of %lld tokens do not fit a workspace",
+                (long long)tree->length);
   return rc != 0 ? cuda_fail(rc, "attention weights") : RECSA_OK;
 }
 

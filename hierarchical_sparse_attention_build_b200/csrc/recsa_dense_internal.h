@@ -21,7 +21,7 @@ constexpr size_t kDensePrefix = kDenseRedo + kMaxShared * sizeof(uint32_t);  // 
 constexpr size_t kDensePart = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
-constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a weights call
+constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a call that keeps their scores
 constexpr size_t kDenseImages = kDenseLse + kMaxDenseLse * sizeof(float);   // rotated rows of a chunk's keys and queries
 constexpr size_t kMaxDenseImages = (size_t)320 << 20;   // for many heads together
 constexpr size_t kMaxHeadImages = (size_t)1280 << 20;   // for one long head
@@ -66,8 +66,8 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
 constexpr int kNoRoom = -1000;
 int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, int64_t image_bytes, void *stream);
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
-// Weights per slot; `lse` has a float for each query row; kNoRoom, with nothing launched, where one
-// head's rotated rows do not fit `room` bytes of images.
+// Weights per slot; `lse` has room for kMaxDenseLse floats; kNoRoom, with nothing launched, where
+// one head's rotated keys do not fit `room` bytes of images.
 int launch_dense_weights(const DenseArgs &a, float *lse, float *weights, int accumulate, int64_t room, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
                          int count, int64_t limit, void *stream);

@@ -33,7 +33,8 @@ constexpr int kTurnRows = 32;               // query rows a block of the images 
 struct ScoreArgs {
   DenseArgs d;
   int bh0, heads;              // the launch's (sequence, KV head) pairs
-  int row_tiles, key_tiles;    // of a head: 128 query rows, 128 keys
+  int row0, row_tiles;         // and the query rows of each: from row0 on, in tiles of 128
+  int key_tiles;               // of a head, 128 keys
   int nsplit;
   unsigned char *key_images, *query_images;  // [heads][key_tiles], [heads][row_tiles]: two parts each
   uint4 *live;                 // a key tile's tokens that were loaded
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(Sco
     const int len = dense_length(d, b, false);
 #pragma unroll
     for (int i = 0; i < kTurnRows / 16; ++i) {
-      const int in_tile = e % kParts * kTurnRows + r0 + 16 * i, row = rt * kTile + in_tile, qi = row >> gs;
+      const int in_tile = e % kParts * kTurnRows + r0 + 16 * i, row = a.row0 + rt * kTile + in_tile, qi = row >> gs;
       uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
       if (qi < d.nq) {
         const uint4 *src =
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   auto wait = [&](uint64_t *bar, uint32_t parity) { bounded_wait(&sm.stop, d.hdr, bar, parity); };
   // key tiles that row tile rt's queries see (at least one, so that every row tile has a product)
   auto last_tile = [&](int rt) {
-    const int row = min((rt + 1) * kTile, d.nq << d.group_shift) - 1;
+    const int row = min(a.row0 + (rt + 1) * kTile, d.nq << d.group_shift) - 1;
     const int p = row_position(d, len, row);
     return max(kt0 + 1, min(kt1, (max(p, 0) + kTile - 1) / kTile));
   };
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
       if (PASS == 2) {
         asm volatile("bar.sync 1, 256;" ::: "memory");  // the last row tile's values have been read
         if (tid < kTile) {
-          const int p = row_position(d, len, rt * kTile + tid);
+          const int p = row_position(d, len, a.row0 + rt * kTile + tid);
           const float2 *src = a.sums + ((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) * kTile + tid;
           float m = -INFINITY, l = 0.f;
           for (int j = 0; j < 2 * a.nsplit; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
@@ -233,13 +234,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
             if (v.x != -INFINITY) l += v.y * exp2_approx(v.x - m);
           }
           // a row that sees nothing gives no weight; neither does a row past the queries
-          sm.lse[tid] = (rt * kTile + tid) < (d.nq << d.group_shift) && (l > 0.f || l != l) ? m + log2f(l) : INFINITY;
+          sm.lse[tid] = a.row0 + rt * kTile + tid < (d.nq << d.group_shift) && (l > 0.f || l != l) ? m + log2f(l) : INFINITY;
           sm.pos[tid] = p;
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
       }
-      const int p_row = PASS == 1 ? row_position(d, len, rt * kTile + trow) : 0;
-      const int p_least = row_position(d, len, rt * kTile);  // positions grow with the row
+      const int p_row = PASS == 1 ? row_position(d, len, a.row0 + rt * kTile + trow) : 0;
+      const int p_least = row_position(d, len, a.row0 + rt * kTile);  // positions grow with the row
       float m = -INFINITY, l = 0.f;
       for (int kt = kt0; kt < end; ++kt, ++n) {
         if ((int)(n & 1) != set) continue;
@@ -247,14 +248,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
         const uint4 live = __ldg(a.live + (int64_t)hl * a.key_tiles + kt);
         wait(&sm.d_full[set], (n >> 1) & 1);
         umma::fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) umma::tmem_ld32(td + g * 32, s[g]);
-        umma::tmem_wait_ld();
-        umma::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.d_empty[set]);
+        auto taken = [&]() {  // the accumulator may be overwritten
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.d_empty[set]);
+        };
         if (PASS == 1) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) umma::tmem_ld32(td + g * 32, s[g]);
+          umma::tmem_wait_ld();
+          taken();
           const uint32_t lv[4] = {live.x, live.y, live.z, live.w};
           if (T + kTile > p_row || (live.x & live.y & live.z & live.w) != 0xffffffffu) {
 #pragma unroll
@@ -285,14 +289,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           const uint32_t lw = trow < 32 ? live.x : trow < 64 ? live.y : trow < 96 ? live.z : live.w;
           const bool whole = T + kTile <= p_least;
           float add[4] = {};
+          uint32_t s[2][32];
+          umma::tmem_ld32(td, s[0]);
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
+          for (int g = 0; g < 4; ++g) {  // 32 columns, the next 32 on their way
+            umma::tmem_wait_ld();
+            if (g < 3)
+              umma::tmem_ld32(td + (g + 1) * 32, s[(g + 1) & 1]);
+            else
+              taken();
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float4 z = *reinterpret_cast<const float4 *>(&sm.lse[g * 32 + i]);
-              float e[4] = {exp2_approx(__uint_as_float(s[g][i]) - z.x), exp2_approx(__uint_as_float(s[g][i + 1]) - z.y),
-                            exp2_approx(__uint_as_float(s[g][i + 2]) - z.z),
-                            exp2_approx(__uint_as_float(s[g][i + 3]) - z.w)};
+              const uint32_t *u = &s[g & 1][i];
+              float e[4] = {exp2_approx(__uint_as_float(u[0]) - z.x), exp2_approx(__uint_as_float(u[1]) - z.y),
+                            exp2_approx(__uint_as_float(u[2]) - z.z), exp2_approx(__uint_as_float(u[3]) - z.w)};
               if (!whole) {
                 const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 32 + i]);
                 if (t >= p.x) e[0] = 0.f;
@@ -303,6 +314,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
 #pragma unroll
               for (int k = 0; k < 4; ++k) add[k] += e[k];
             }
+          }
           if ((lw >> (trow & 31)) & 1u) sm.acc[(kt - kt0) * kTile + trow] += (add[0] + add[1]) + (add[2] + add[3]);
         }
       }
@@ -424,45 +436,50 @@ int few_rows(DenseArgs d, float *lse, float *weights, int accumulate, int64_t ro
 
 int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int accumulate, int64_t room, void *stream) {
   const int64_t rows = (int64_t)d.nq << d.group_shift, heads = (int64_t)d.batch * d.hkv;
-  if (rows <= 8) {
+  if (rows <= 8 && rows * heads <= kMaxDenseLse) {
     const int rc = few_rows(d, lse, weights, accumulate, room, stream);
     if (rc != kNoRoom) return rc;
   }
   ScoreArgs a = {};
   a.d = d;
   a.weights = weights;
-  a.accumulate = accumulate;
-  a.row_tiles = (int)ceil_div(rows, kTile);
   a.key_tiles = (int)ceil_div(std::max(d.length, 1), kTile);
-  const int64_t head_bytes = a.key_tiles * (int64_t)(kPartBytes + sizeof(uint4)) + a.row_tiles * (int64_t)kPartBytes;
-  const int64_t fit = room / head_bytes;
-  if (fit < 1) return kNoRoom;
   cudaError_t e = cudaFuncSetAttribute(dense_scores_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e != cudaSuccess) return (int)e;
   const cudaStream_t st = (cudaStream_t)stream;
   const int sms = dense_sm_count();
-  // the sums of a head's rows, once for each part of the keys
-  const int64_t least = ceil_div(a.key_tiles, kMaxRange);
-  const int64_t sums_room = (int64_t)kDensePartBytes / (a.row_tiles * 2 * (int64_t)(kTile * sizeof(float2)));
-  if (sums_room < least) return kNoRoom;
-  const int64_t step = std::min({heads, fit, sums_room / least});
+  // As many heads and rows a launch as the images' room and the sums' hold: an eighth of the room
+  // for one head's rows, at least one tile of them.  Later rows add to what earlier ones wrote.
+  const int64_t key_bytes = a.key_tiles * (int64_t)(kPartBytes + sizeof(uint4)), least = ceil_div(a.key_tiles, kMaxRange);
+  const int64_t sums = (int64_t)kDensePartBytes / (2 * (int64_t)(kTile * sizeof(float2)));  // of a row tile and a part
+  const int64_t all_tiles = ceil_div(rows, kTile);
+  const int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, std::min(room / 8 / kPartBytes, sums / least)));
+  const int64_t fit = std::min(room / (key_bytes + tiles * (int64_t)kPartBytes), sums / (least * tiles));
+  if (fit < 1) return kNoRoom;
+  const int64_t step = std::min(heads, fit);
   for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
     a.bh0 = (int)bh0;
     a.heads = (int)std::min(step, heads - bh0);
-    // one wave of blocks where that leaves each at most kMaxRange key tiles
-    a.nsplit = (int)std::min<int64_t>({std::max<int64_t>(least, sms / a.heads), a.key_tiles, sums_room / a.heads});
     a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
     a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kPartBytes;
-    a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * a.row_tiles * kPartBytes);
+    a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * tiles * kPartBytes);
     a.sums = reinterpret_cast<float2 *>(reinterpret_cast<char *>(d.hdr) + kDensePart);
-    const int64_t blocks = (int64_t)a.heads * (a.key_tiles + (int64_t)a.row_tiles * (kTile / kTurnRows));
-    dense_score_images_kernel<<<(unsigned)blocks, kTurnThreads, 0, st>>>(a);
-    dense_scores_kernel<1><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
-    dense_scores_kernel<2><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return (int)e;
+    for (int64_t rt0 = 0; rt0 < all_tiles; rt0 += tiles) {
+      a.row0 = (int)(rt0 * kTile);
+      a.row_tiles = (int)std::min(tiles, all_tiles - rt0);
+      a.accumulate = accumulate || rt0 > 0;
+      // one wave of blocks where that leaves each at most kMaxRange key tiles
+      a.nsplit = (int)std::min<int64_t>(
+          {std::max<int64_t>(least, sms / a.heads), a.key_tiles, sums / ((int64_t)a.heads * a.row_tiles)});
+      const int64_t blocks = (int64_t)a.heads * (a.key_tiles + (int64_t)a.row_tiles * (kTile / kTurnRows));
+      dense_score_images_kernel<<<(unsigned)blocks, kTurnThreads, 0, st>>>(a);
+      dense_scores_kernel<1><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
+      dense_scores_kernel<2><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return (int)e;
+    }
   }
   return 0;
 }

@@ -55,7 +55,8 @@ typedef struct recsa_view {
   int32_t kernel;
 } recsa_view;
 
-/* Bytes of the workspace of the dense calls on caches of `batch` sequences of up to
+/* Bytes of the workspace (about 48 MB, and up to 320 MB - for sequences of more than 1.2 million
+ * tokens up to 1.25 GB - for the rotated rows of long chunks) of the dense calls on caches of `batch` sequences of up to
  * `capacity` tokens (host only).  Unlike recsa_decode's, this workspace is written by every
  * call (partial sums of sequences that several thread blocks share), so calls whose GPU work
  * can overlap - other streams, two captured graphs replayed side by side - each need their
@@ -105,7 +106,8 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
  * and over the query heads of its KV group, in fp32.
  *   weights : fp32 [batch][Hkv][capacity]; slots [0, L) are overwritten (accumulate = 0) or
  *             added to (accumulate = 1), slots at or past a sequence's L are left as they are.
- * Views with a window are RECSA_ERR_UNSUPPORTED. */
+ * Views with a window are RECSA_ERR_UNSUPPORTED, and so are more than 8 query rows a KV group
+ * over sequences of more than about 2.5 million tokens (their rotated keys do not fit). */
 RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, const recsa_tree *tree,
                                                 const recsa_view *view, const void *q, int32_t num_queries,
                                                 float *weights, int32_t accumulate, void *ws, size_t ws_bytes,

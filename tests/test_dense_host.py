@@ -102,7 +102,7 @@ def test_counts_and_room():
     refused(INVALID, *call("step"))  # no per-sequence lengths
     refused(INVALID, *call("step", t=T(seq_len=FAKE), k=None))
     refused(UNSUPPORTED, *call("weights", view=R.View(window=8)))
-    refused(UNSUPPORTED, *call("weights", n=1 << 19))  # more rows than the workspace has sums for
+    refused(UNSUPPORTED, *call("weights", n=(1 << 31) - 1))
     refused(UNSUPPORTED, *call("attend", n=(1 << 31) - 1))
     assert R.View(sinks=3, window=9, causal=True, own_token=True, token_positions=True).sink_positions == 1
 

@@ -433,6 +433,54 @@ def test_chunks(case):
         assert torch.equal(got, c.attend(False, v))
 
 
+def test_empty_caches():
+    c = Case(2, 2, 4, 1, 3, seed=80, spare=40)
+    c.cache.length = 0
+    for fp32, kernel in ((True, R.DENSE_ROWS), (False, R.DENSE_ROWS), (False, R.DENSE_CHUNK)):
+        for view in (R.View(kernel=kernel), R.View(causal=True, own_token=True, kernel=kernel)):
+            assert not c.attend(fp32, view).any()
+    w = torch.full((2, 2, c.cap), 3.0, device="cuda")
+    R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws)
+    kept = torch.zeros(2, 2, 5, dtype=torch.int32, device="cuda")
+    R.evict(c.p, c.cache, w, 5, kept)
+    R.check_device_errors(c.ws)
+    assert (w == 3.0).all() and (kept == -1).all() and c.cache.length == 0
+
+
+def test_more_queries_than_the_images_hold():
+    """A short cache's workspace holds the rotated rows of a few items at a time."""
+    c = Case(1, 1, 8, 128, 700, seed=81)
+    check(c.attend(False, R.View(kernel=R.DENSE_CHUNK)), c.want(), False, 0.0)
+    want = c.want(want_weights=True)
+    w = torch.full((1, 1, c.cap), 0.5, device="cuda")
+    for acc in (False, True):
+        R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws, accumulate=acc)
+        assert float((w.double().cpu() / (1 + acc) - want).norm() / want.norm()) <= 2.0 ** -16
+
+
+def test_more_heads_than_the_images_hold():
+    """Long caches whose heads' rotated keys do not fit the workspace together: heads in turn."""
+    H, G, L, n = 8, 4, 180001, 80
+    p = params(H, G)
+    g = torch.Generator(device="cuda").manual_seed(82)
+    k, v = (torch.empty(1, H, L, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    q = torch.empty(1, n, H * G, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    cache, ws = R.TokenCache(p, k, v, L), R.DenseWorkspace(p, 1, L, "cuda")
+    assert ws.nbytes < 8 * L * 256 + (50 << 20)
+    view = R.View(causal=True, own_token=True, kernel=R.DENSE_CHUNK)
+    out = torch.empty_like(q)
+    R.dense_attend(p, cache, q, out, ws, view)
+    w = torch.zeros(1, H, L, device="cuda")
+    R.accumulate_weights(p, cache, q[:, -8:].contiguous(), w, ws, view)
+    R.check_device_errors(ws)
+    for h in (0, 3, 6, 7):
+        one = dict(q=q[:, -8:, h * G:(h + 1) * G], k=k[:, h:h + 1], v=v[:, h:h + 1], lens=[L], G=G, base=BASE, causal=True,
+                   own=True)
+        check(out[:, -8:, h * G:(h + 1) * G], F.attend(**one).cpu(), False, 0.0)
+        want = F.attend(want_weights=True, **one)
+        assert float((w[:, h:h + 1].double() - want).norm() / want.norm()) <= 2.0 ** -16
+
+
 def test_chunk_rows_beyond_half_precision():
     """Keys or queries larger than fp16 holds: the tile is computed by the rows kernel."""
     for big_q in (False, True):
