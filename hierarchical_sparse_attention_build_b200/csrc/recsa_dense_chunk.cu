@@ -16,8 +16,8 @@
 //   warp 13        : one thread copies the images.
 // While one row tile's softmax runs, the tensor cores do the other's O += P V and next S.
 //
-// Rounding: rotated queries and keys are rounded to fp16 (half a step is 2^-12 of an element:
-// an eighth of what bf16 would add to a score), probabilities to bf16 (the values' type: one
+// Rounding: rotated queries and keys are rounded to fp16 (half a step is 2^-11 of an element, an
+// eighth of bf16's), probabilities to bf16 (the values' type: one
 // product takes one type; half a step, 2^-8 of a weight, as the output's own rounding).  A
 // rotated element beyond fp16's range, or an output that is not finite (a hidden token's value
 // may hold anything, and a zero weight times infinity is NaN), marks the item: the rows kernel,

@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
         } else {
           const int t = T + trow;
           const uint32_t lw = trow < 32 ? live.x : trow < 64 ? live.y : trow < 96 ? live.z : live.w;
-          const bool whole = T + kTile <= p_least;
+          // every row of the tile is a query's, and sees every key of the tile
+          const bool whole = T + kTile <= p_least && a.row0 + (rt + 1) * kTile <= d.nq << d.group_shift;
           float add[4] = {};
           uint32_t s[2][32];
           umma::tmem_ld32(td, s[0]);
@@ -393,10 +394,13 @@ __global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, c
   const int bh = a.bh0 + blockIdx.y, b = bh / a.hkv, h = bh % a.hkv, gs = a.group_shift, G = 1 << gs;
   const int len = dense_length(a, b, false), rows = a.nq << gs;
   __shared__ float z[8];
-  if (threadIdx.x < 8)
+  __shared__ int pos[8];  // the rows kernel visits no token that no row sees
+  if (threadIdx.x < 8) {
+    pos[threadIdx.x] = threadIdx.x < rows ? dense_position(a, len, threadIdx.x >> gs) : 0;
     z[threadIdx.x] = threadIdx.x < rows ? lse[((int64_t)b * a.nq + (threadIdx.x >> gs)) * (a.hkv << gs) + h * G +
                                               (threadIdx.x & (G - 1))]
                                         : INFINITY;
+  }
   __syncthreads();
   const float *s = a.scores + (int64_t)blockIdx.y * a.score_pitch * a.score_stride;
   float *const w = weights + ((int64_t)b * a.hkv + h) * a.capacity;
@@ -404,8 +408,8 @@ __global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, c
     float v = 0.f;
     for (int i = 0; i < a.score_stride; i += 2) {
       const float2 x = __ldcs(reinterpret_cast<const float2 *>(s + (int64_t)t * a.score_stride + i));
-      if (i < rows) v += exp2_approx(x.x - z[i]);
-      if (i + 1 < rows) v += exp2_approx(x.y - z[i + 1]);
+      if (t < pos[i]) v += exp2_approx(x.x - z[i]);
+      if (t < pos[i + 1]) v += exp2_approx(x.y - z[i + 1]);
     }
     w[t] = accumulate ? w[t] + v : v;
   }

@@ -535,6 +535,27 @@ def test_weights(B, H, G, L, n, page, lens, view):
         assert (twice[b, :, m:] == 3.0).all()
 
 
+@pytest.mark.parametrize("B,G,L,n,lens", [
+    (1, 2, 4097, 2, None),  # the last token is seen by no query and opens a step of its own
+    (2, 1, 33, 8, [33, 1]),
+    (2, 4, 16, 1, [1, 16]),
+    (1, 4, 385, 20, None),  # the same in the kernel for more rows
+])
+def test_weights_of_tokens_no_query_sees(B, G, L, n, lens):
+    """Without its own token a chunk's last one is seen by none: its weight is 0, whatever an
+    earlier call left in the workspace."""
+    c = Case(B, 2, G, L, n, seed=90, lens=lens)
+    c.ws.buf[1 << 20:] = 0x41
+    w = torch.full((B, 2, c.cap), 3.0, device="cuda")
+    R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws, R.View(causal=True), accumulate=False)
+    R.check_device_errors(c.ws)
+    want = c.want(causal=True, want_weights=True)
+    for b, m in enumerate(c.lens):
+        got = w[b, :, :m].double().cpu()
+        assert (got[:, m - 1] == 0).all()
+        assert float((got - want[b, :, :m]).norm()) <= 2.0 ** -16 * max(float(want[b, :, :m].norm()), 1.0)
+
+
 # ---------------------------------------------------------------------------- eviction
 
 
