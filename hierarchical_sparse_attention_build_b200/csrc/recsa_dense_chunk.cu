@@ -39,7 +39,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kLoadThreads = 128;
 constexpr int kChunkThreads = 512;
 constexpr int kQueryBytes = 2 * kTileBytes;
-constexpr int kQueryRows = 32;              // query rows a block of the images kernel turns
+constexpr int kQueryRows = 64;              // query rows a block of the images kernel turns
 constexpr int kRing = 2;                    // key and value tiles in shared memory
 constexpr int kMaxChunkBlocks = (int)(kDensePartBytes / (2 * kItemRows * kPartRow * sizeof(float)));
 constexpr float kRescale = 64.f;            // a row's maximum may lag by 2^64 before its output is rescaled
@@ -183,23 +183,46 @@ __device__ __forceinline__ void wait(ChunkSmem &sm, const ChunkArgs &a, uint64_t
 __device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *q, const Item &it, bool sink, int row0,
                                              int lt, __half2 &most) {
   const DenseArgs &d = a.d;
-  const int ch = lt & 7, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
+  const int ch = lt & 7, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs, r0 = row0 + (lt >> 3);
+  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
+  constexpr int kPer = kQueryRows / 16;  // rows r0 + 16 i of a thread
+  auto position = [&](int i) {
+    const int p = dense_position(d, it.len, it.q0 + ((r0 + 16 * i) >> gs));
+    return sink ? sink_position(d, p) : p;
+  };
+  uint4 lo[kPer], hi[kPer];
 #pragma unroll
-  for (int i = 0; i < kQueryRows / 16; ++i) {
-    const int row = row0 + (lt >> 3) + 16 * i, qi = row >> gs;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  for (int i = 0; i < kPer; ++i) {
+    const int row = r0 + 16 * i, qi = row >> gs;
+    lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
     if (qi < it.nq) {
       const uint4 *src = reinterpret_cast<const uint4 *>(
           d.q + (((int64_t)it.b * d.nq + it.q0 + qi) * hq + it.h * G + (row & (G - 1))) * kD);
-      lo = __ldg(src + ch);
-      hi = __ldg(src + ch + 8);
+      lo[i] = __ldg(src + ch);
+      hi[i] = __ldg(src + ch + 8);
     }
-    const int p = dense_position(d, it.len, it.q0 + qi);
-    Turn t;
-    t.set(ws_freq(d.hdr) + ch * 8, sink ? sink_position(d, p) : p);
+  }
+  // the rows' positions advance evenly (16 / G a step, or not at all), except where the sinks'
+  // positions stop growing on the way: those are turned one by one
+  const int p0 = position(0), by = position(1) - p0;
+  bool even = true;
+#pragma unroll
+  for (int i = 2; i < kPer; ++i) even = even && position(i) == p0 + i * by;
+  Turn t, step;
+  t.set(f, p0);
+  if (by != 0) step.set(f, by);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int row = r0 + 16 * i;
     uint4 ol, oh;
-    turn_row<true>(lo, hi, t, d.qscale, ol, oh, most);
+    turn_row<true>(lo[i], hi[i], t, d.qscale, ol, oh, most);
     put_row(q + (row >> 7) * kTileBytes, row & 127, ch, ol, oh);
+    if (i + 1 < kPer) {
+      if (!even)
+        t.set(f, position(i + 1));
+      else if (by != 0)
+        t.advance(step);
+    }
   }
 }
 
