@@ -7,21 +7,25 @@
 //
 // dense_chunk_kernel: a work item is 256 query rows (256 / G queries x the G heads of one KV
 // group) of one sequence, as two tiles of 128 rows; its keys come in tiles of 128.  One CTA per SM:
-//   warps 0-3, 4-7 : softmax of the two row tiles, a thread a row with its 128 scores in
-//                    registers; the probabilities go over the scores in TMEM.  (Two threads a row
-//                    were slower: their exchange of maxima cost more than the shorter rows gave.)
+//   warps 0-3, 4-7 : softmax of the two row tiles, a thread a row with 64 scores in registers; the
+//                    probabilities go over the scores in TMEM.  (Two threads a row were slower:
+//                    their exchange of maxima cost more than the shorter rows gave.)
 //   warps 8-11     : gather the values with cp.async (any page size) into swizzled tiles;
-//   warp 12        : one thread issues the products S = Q K^T (shared x shared) and O += P V
-//                    (TMEM x shared) of the two row tiles in turn;
+//   warps 12, 14   : one thread each issues a row tile's products, S = Q K^T (shared x shared) and
+//                    O += P V (TMEM x shared).  (One thread for both spent 200 cycles a wait with
+//                    the tensor cores idle.)
 //   warp 13        : one thread copies the images.
-// While one row tile's softmax runs, the tensor cores do the other's O += P V and next S.
+// Steps are half a key tile, 64 keys: a row's softmax has one half while the tensor cores do the
+// other half's O += P V and next S, and the other row tile's.
+// Measured: 2048 queries over 16384 tokens, 32/8 heads: 465 us, 1108 TFLOP/s, tensor pipe and
+// special-function unit each half busy; 4096 over 32768: 2.0 ms in a short burst, 2.3 ms at the
+// power limit.  What bounds it is the wait of a row's next scores for its weights and back.
 //
 // Rounding: rotated queries and keys are rounded to fp16 (half a step is 2^-11 of an element, an
-// eighth of bf16's), probabilities to bf16 (the values' type: one
-// product takes one type; half a step, 2^-8 of a weight, as the output's own rounding).  A
-// rotated element beyond fp16's range, or an output that is not finite (a hidden token's value
-// may hold anything, and a zero weight times infinity is NaN), marks the item: the rows kernel,
-// which has neither limit, then computes it again.
+// eighth of bf16's), probabilities to bf16 (the values' type: one product takes one type; half a
+// step, 2^-8 of a weight, as the output's own rounding).  A rotated element beyond fp16's range, or
+// an output that is not finite (a hidden token's value may hold anything, and a zero weight times
+// infinity is NaN), marks the item: the rows kernel, which has neither limit, then computes it again.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -399,8 +403,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) dense_chunk_kernel(ChunkArgs
   Segments sg = segments_begin(a, sm);
   Item it;
 
-  // Registers a thread: 512 threads are launched with 128 (65,536); the softmax takes 176, the
-  // loaders 64 and the last four warps 96 of them (65,536).
+  // Registers a thread: 512 threads are launched with 128 (65,536); the softmax takes 144, the
+  // loaders give theirs down to 96 and the last four warps keep 128 (65,536).
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax and epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");

@@ -305,6 +305,48 @@ def test_decode_steps_and_their_graph(view):
         check(got[0][i], c.want(sinks=view.sinks, window=view.window), True, c.bound())
 
 
+def test_captured_calls_replay():
+    """A chunk, the weights of many and of few rows, and an eviction captured once: replays give the
+    eager calls' bits on new inputs, also after eager calls on the same workspace."""
+    B, H, G, L, n, keep = 2, 2, 4, 700, 90, 200
+    c = Case(B, H, G, L, n, seed=37, lens=[700, 350])
+    into = R.TokenCache(c.p, *(torch.zeros(B, H, keep, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)), 0,
+                        seq_len=torch.zeros(B, dtype=torch.int64, device="cuda"))
+    view, few = R.View(causal=True, own_token=True, kernel=R.DENSE_CHUNK), R.View(causal=True)
+    out = torch.empty_like(c.qd)
+    q1 = c.qd[:, -2:].contiguous()
+    w, w1 = (torch.zeros(B, H, c.cap, device="cuda") for _ in range(2))
+    kept = torch.empty(B, H, keep, dtype=torch.int32, device="cuda")
+
+    def calls():
+        R.dense_attend(c.p, c.cache, c.qd, out, c.ws, view)
+        R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws, view, accumulate=False)
+        R.accumulate_weights(c.p, c.cache, q1, w1, c.ws, few, accumulate=False)
+        R.evict(c.p, c.cache, w, keep, kept, into=into, sinks=2, recent=8)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        calls()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(3):
+        c.qd.normal_()
+        q1.copy_(c.qd[:, -2:])
+        c.cache.seq_len.copy_(torch.randint(1, L, (B,)))
+        c.cache.k_tok.normal_()
+        results = []
+        for run in (graph.replay, calls):
+            for t in (out, w, w1, kept, into.k_tok, into.seq_len):
+                t.zero_()
+            run()
+            results.append([t.clone() for t in (out, w, w1, kept, into.k_tok, into.v_tok, into.seq_len)])
+        assert all(torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float())) for a, b in zip(*results))
+    R.check_device_errors(c.ws)
+
+
 def test_a_full_sequence_is_flagged_and_kept():
     c = Case(2, 1, 2, 32, 1, seed=33, lens=[32, 10])
     before = c.cache.k_tok.clone()
