@@ -325,8 +325,10 @@ class View(ctypes.Structure):
 
     window = 0 sees every token before the query; otherwise the last `window` tokens and the
     first `sinks`.  causal: the queries belong to the cache's last tokens (else all sit at its
-    end); own_token: a causal query also sees its own token.  token_positions: sinks outside
-    the window are scored at their token positions instead of their rank among the visible.
+    end); own_token: a causal query also sees its own token, from one position past it;
+    at_token: it sees it and sits at its position (a query at the cache's end: at the last
+    token's), as the layers of a causal RoPE model do.  token_positions: sinks outside the
+    window are scored at their token positions instead of their rank among the visible.
     kernel: DENSE_AUTO, DENSE_ROWS or DENSE_CHUNK."""
 
     _fields_ = [
@@ -339,8 +341,8 @@ class View(ctypes.Structure):
     ]
 
     def __init__(self, sinks: int = 0, window: int = 0, causal: bool = False, own_token: bool = False,
-                 token_positions: bool = False, kernel: int = 0):
-        super().__init__(sinks, window, int(token_positions), int(causal), int(own_token), kernel)
+                 token_positions: bool = False, kernel: int = 0, at_token: bool = False):
+        super().__init__(sinks, window, int(token_positions), int(causal), 2 if at_token else int(own_token), kernel)
 
 
 class TokenCache(RecsaTree):

@@ -46,13 +46,14 @@ __device__ __forceinline__ int dense_length(const DenseArgs &a, int b, bool repo
   return (int)n;
 }
 
-// Position of query i of a sequence of len tokens; 0 or less: it sees nothing.
+// The p of query i of a sequence of len tokens: it sees tokens t < p (0 or less: nothing) and sits
+// at p - back.
 __device__ __forceinline__ int dense_position(const DenseArgs &a, int len, int i) {
   return a.causal ? len - a.nq + i + a.own : len;
 }
-// Position a query at p has for the sinks (those outside its window).
+// Where a query of bound p sits for the sinks (those outside its window).
 __device__ __forceinline__ int sink_position(const DenseArgs &a, int p) {
-  return a.rank_sinks ? min(p, a.sinks + a.window) : p;
+  return (a.rank_sinks ? min(p, a.sinks + a.window) : p) - a.back;
 }
 // The tokens a query at p sees, besides the first min(sinks, p): [first, p).
 __device__ __forceinline__ int window_first(const DenseArgs &a, int p) {

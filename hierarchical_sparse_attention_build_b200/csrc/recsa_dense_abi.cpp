@@ -31,6 +31,7 @@ recsa_status check_view(const recsa_view *v) {
   if (v->kernel < 0 || v->kernel > 2) return fail(RECSA_ERR_INVALID_ARGUMENT, "kernel %d (0 .. 2)", v->kernel);
   if (v->sink_positions != 0 && v->sink_positions != 1)
     return fail(RECSA_ERR_INVALID_ARGUMENT, "sink_positions %d (0 or 1)", v->sink_positions);
+  if (v->own_token < 0 || v->own_token > 2) return fail(RECSA_ERR_INVALID_ARGUMENT, "own_token %d (0 .. 2)", v->own_token);
   return RECSA_OK;
 }
 
@@ -77,6 +78,7 @@ DenseArgs dense_args(const recsa_params *p, const recsa_tree *t, const recsa_vie
   }
   a.causal = causal;
   a.own = causal && own;
+  a.back = v && v->own_token == 2;
   a.nsplit = a.tiles = 1;
   a.qscale = (p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)kD)) * kLog2e;
   a.rope_base = p->rope_base;

@@ -192,7 +192,7 @@ __device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *
   constexpr int kPer = kQueryRows / 16;  // rows r0 + 16 i of a thread
   auto position = [&](int i) {
     const int p = dense_position(d, it.len, it.q0 + ((r0 + 16 * i) >> gs));
-    return sink ? sink_position(d, p) : p;
+    return sink ? sink_position(d, p) : p - d.back;
   };
   uint4 lo[kPer], hi[kPer];
 #pragma unroll

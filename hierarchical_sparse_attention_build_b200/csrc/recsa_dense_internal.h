@@ -40,6 +40,7 @@ struct DenseArgs {
   int32_t batch, hkv, group_shift, nq;
   int32_t length;
   int32_t sinks, window, rank_sinks, causal, own;
+  int32_t back;       // a query that sees the tokens t < p sits at p - back
   int32_t out_fp32;
   int32_t tiles, nsplit;
   float qscale;       // softmax scale * log2(e)

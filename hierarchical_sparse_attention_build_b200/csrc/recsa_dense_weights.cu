@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(Sco
         hi = __ldg(src + ch + 8);
       }
       Turn t;
-      t.set(f, dense_position(d, len, qi));
+      t.set(f, dense_position(d, len, qi) - d.back);
       put_parts<true>(a.query_images + (int64_t)image * kPartBytes, in_tile, ch, lo, hi, t, d.qscale);
     }
     return;

@@ -20,6 +20,10 @@
  * t < sinks and p - window <= t < p.  Scores are softmax_scale * <R_p q, R_t k_t> with the
  * rotate-half RoPE R of recsa.h; a sink that lies outside the window is scored at its rank
  * among the visible tokens (the query then sits at sinks + window), or at its token position.
+ * So p counts the tokens that a query sees, as in recsa_decode: a query that sees its own
+ * token, at position p - 1, still sits one past it.  A causal RoPE layer has the query at its
+ * own token instead, <R_i q_i, R_t k_t> for t <= i: recsa_view.own_token = 2.  The query of
+ * bound p then sits at p - 1 (for the sinks at sinks + window - 1), in every call here.
  * The output is the softmax-weighted mean of the visible values; a query that sees nothing
  * outputs zeros.  Rows that a query does not see never reach its output, whatever they hold.
  */
@@ -39,8 +43,11 @@ extern "C" {
  *                    tokens; 1 = at its token position.
  *   causal         : 0 = every query sits at p = L (decode); 1 = the n queries belong to the
  *                    last n tokens of the cache: query i sits at p = L - n + i.
- *   own_token      : with causal: 1 = a query also sees its own token (p = L - n + i + 1).
- *                    0 is the position convention of recsa_prefill_chunk.
+ *   own_token      : with causal: 1 or 2 = a query also sees its own token
+ *                    (p = L - n + i + 1); 0 is the position convention of recsa_prefill_chunk.
+ *                    2, causal or not: a query sits at p - 1, its own token's position (that
+ *                    of the cache's last token for queries at the end, and in a decode step):
+ *                    the attention of a dense or windowed RoPE layer.
  *   kernel         : launch-shape override of the attention calls: 0 = automatic by the sizes;
  *                    1 = the rows kernel (8 or 16 query rows a block; every output type);
  *                    2 = the chunk kernel (256 query rows a block on tcgen05; bf16 outputs,
@@ -96,7 +103,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
  * included).  Every launch parameter comes from the capacity, so the call can be captured into
  * a CUDA graph.  Needs tree->seq_len; tree->length is neither read nor written.  A sequence
  * with no room keeps its tokens and length and is flagged (RECSA_ERR_DEVICE_CHECK).
- * view->causal and own_token are not used. */
+ * view->causal is not used; own_token = 2 puts the query at its own token's position. */
 RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const recsa_tree *tree,
                                                const recsa_view *view, const void *k_new, const void *v_new,
                                                const void *q, void *out, int32_t out_is_fp32, void *ws,

@@ -159,3 +159,13 @@ def test_binding_refuses_wrong_tensors():
         R._weights_of(c, z(2, 2, 64, dt=torch.float64), "weights")
     with pytest.raises(R.RecsaError):
         R.DenseWorkspace(p, 2, 64, "cpu")
+
+
+def test_own_token_values():
+    assert [R.View(own_token=o, at_token=t).own_token for o, t in ((False, False), (True, False), (True, True),
+                                                                   (False, True))] == [0, 1, 2, 2]
+    for bad in (-1, 3):
+        v = R.View()
+        v.own_token = bad
+        for op in OPS:
+            refused(INVALID, *call(op, t=T(seq_len=FAKE), view=v))
