@@ -475,7 +475,9 @@ def evict(p: Params, tree: RecsaTree, weights: torch.Tensor, keep: int, kept: to
           into: RecsaTree | None = None, into_weights: torch.Tensor | None = None, sinks: int = 0, recent: int = 0,
           stream=None) -> None:
     """recsa_evict: cut every (sequence, KV head) to its `keep` heaviest slots, in place or into
-    another cache; kept [B][Hkv][keep] int32 receives the kept slots."""
+    another cache; kept [B][Hkv][keep] int32 receives the kept slots, into_weights their weights
+    (in place, 0 in the slots given up; beside another cache the slots past the kept ones are
+    left as they are: clear a buffer that was used before)."""
     _weights_of(tree, weights, "weights")
     if kept.dtype != torch.int32 or not kept.is_contiguous() or tuple(kept.shape) != (tree.batch, p.num_kv_heads, keep):
         raise RecsaError(1, f"kept is {kept.dtype} {tuple(kept.shape)}, not contiguous int32 "

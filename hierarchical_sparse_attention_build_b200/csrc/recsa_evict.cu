@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
         if (j < count) to[j] = x[r];
       }
     }
+    // the next tokens go to the slots behind: they start without the weights of those that are gone
+    for (int j = count + threadIdx.x; j < n; j += kMoveThreads) to[j] = 0.f;
     return;
   }
   uint4 *const rows = col < 4 ? a.to.k : a.to.v;

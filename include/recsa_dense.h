@@ -136,6 +136,10 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
  *                  sequence.  Slots past the kept rows are left as they are.
  *   into_weights : NULL, or fp32 [batch][Hkv][capacity of the receiving cache] that receives
  *                  the kept slots' weights in the same order; in place it may be `weights`.
+ *                  In place the slots from the kept ones up to the old length become 0, so that
+ *                  tokens appended there start from 0 in recsa_accumulate_weights.  Beside
+ *                  another cache, slots past the kept ones are left as they are: a buffer that
+ *                  holds an earlier cache's weights is cleared by the caller before this call.
  * Needs keep >= 1 and sinks + recent <= keep. */
 RECSA_API recsa_status recsa_evict(const recsa_params *params, recsa_tree *tree, const float *weights, int32_t keep,
                                    int32_t sinks, int32_t recent, int32_t *kept, recsa_tree *into,
