@@ -21,6 +21,8 @@ namespace cg = cooperative_groups;
 namespace recsa {
 namespace {
 
+__device__ uint32_t g_evict_err = 0u;  // kErr* (the call takes no workspace); recsa_check_device_errors reads it
+
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
@@ -47,6 +49,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   const int bh = blockIdx.x / nblk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = bh / a.hkv;
   const int n = evict_length(a, b);
+  if (rank == 0 && tid == 0 && evict_bad_length(a, b)) atomicOr(&g_evict_err, kErrIndex);
   int32_t *const kept = a.kept + (int64_t)bh * a.keep;
   if (n <= a.keep) {  // everything stays
     for (int j = rank * kSelThreads + tid; j < a.keep; j += nblk * kSelThreads) kept[j] = j < n ? j : -1;
@@ -190,9 +193,11 @@ __global__ void evict_copy_kernel(EvictArgs a, int64_t *to_len) {
     if (i < 0) continue;
     if (part == 0 && a.to_weights) a.to_weights[bh * a.to_capacity + j] = __ldg(a.weights + bh * a.capacity + i);
     const int64_t src = evict_row(a.from, a.hkv, b, h, i), dst = evict_row(a.to, a.hkv, b, h, j);
-    if (src < 0 || dst < 0) continue;
-    a.to.k[dst * 16 + part] = __ldg(a.from.k + src * 16 + part);
-    a.to.v[dst * 16 + part] = __ldg(a.from.v + src * 16 + part);
+    if ((src < 0 || dst < 0) && part == 0) atomicOr(&g_evict_err, kErrIndex);
+    if (dst < 0) continue;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    a.to.k[dst * 16 + part] = src >= 0 ? __ldg(a.from.k + src * 16 + part) : none;
+    a.to.v[dst * 16 + part] = src >= 0 ? __ldg(a.from.v + src * 16 + part) : none;
   }
 }
 
@@ -244,16 +249,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
       src[r] = dst[r] = -1;
       if (j < count) {
         const int i = kept[j];
-        if (i != j) src[r] = evict_row(a.from, a.hkv, b, h, i), dst[r] = evict_row(a.to, a.hkv, b, h, j);
+        if (i != j) {
+          src[r] = evict_row(a.from, a.hkv, b, h, i);
+          dst[r] = evict_row(a.to, a.hkv, b, h, j);
+          if (src[r] < 0 || dst[r] < 0) atomicOr(&g_evict_err, kErrIndex);
+        }
       }
     }
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r)
-      if (src[r] >= 0) x[r] = rows[src[r] * 16 + part];
+    for (int r = 0; r < kMoveRows; ++r) x[r] = src[r] >= 0 ? rows[src[r] * 16 + part] : make_uint4(0, 0, 0, 0);
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kMoveRows; ++r)
-      if (src[r] >= 0 && dst[r] >= 0) rows[dst[r] * 16 + part] = x[r];
+      if (dst[r] >= 0) rows[dst[r] * 16 + part] = x[r];
   }
 }
 
@@ -264,6 +272,14 @@ __global__ void evict_lengths_kernel(EvictArgs a, int64_t *to_len) {
 }
 
 }  // namespace
+
+int read_evict_errors(uint32_t *bits) {
+  uint32_t v = 0u, zero = 0u;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_evict_err, sizeof(v));
+  if (e == cudaSuccess && v != 0u) e = cudaMemcpyToSymbol(g_evict_err, &zero, sizeof(zero));
+  *bits = v;
+  return (int)e;
+}
 
 int launch_evict(const EvictArgs &a, bool in_place, int64_t *to_len, void *stream) {
   const cudaStream_t st = (cudaStream_t)stream;

@@ -34,6 +34,9 @@ __device__ __forceinline__ int evict_length(const EvictArgs &a, int b) {
   const int64_t n = a.seq_len[b];
   return n < 0 ? 0 : n > a.length ? a.length : (int)n;
 }
+__device__ __forceinline__ bool evict_bad_length(const EvictArgs &a, int b) {
+  return a.seq_len && (a.seq_len[b] < 0 || a.seq_len[b] > a.length);
+}
 // Row of slot t of (sequence, head), or -1 for a page outside the pool.
 __device__ __forceinline__ int64_t evict_row(const EvictCache &c, int hkv, int b, int h, int t) {
   if (!c.pages) return ((int64_t)b * hkv + h) * c.capacity + t;

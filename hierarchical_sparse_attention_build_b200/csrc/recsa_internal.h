@@ -65,6 +65,8 @@ int launch_rope_table(void *ws, int rows, double base, void *stream);
 // Read and clear the build kernels' device error word (kErrTimeout when a wait on the tensor
 // cores gave up); returns a cudaError_t.
 int read_build_errors(uint32_t *bits);
+// The same of the eviction's (kErrIndex: a length or a page-table entry out of range).
+int read_evict_errors(uint32_t *bits);
 int launch_build_level(const TreeGeom &g, const recsa_tree &t, int level, int64_t length, int64_t j0, int64_t j1,
                        void *stream);
 int launch_append(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t at,

@@ -287,7 +287,7 @@ RECSA_API recsa_status recsa_decode_no_alloc(const recsa_params *params, const r
                                              recsa_stream_t stream);
 
 /* Synchronise `stream`, then read and clear the workspace's device error word and the
- * library's own word for the build and append kernels (which take no workspace).
+ * library's own word for the build, append and eviction kernels (which take no workspace).
  * Returns RECSA_OK, RECSA_ERR_DEVICE_CHECK (an index out of range, or a workspace
  * that was not initialised for the call), RECSA_ERR_TIMEOUT (a bounded wait ran
  * out: the attend kernels' none, the build and append kernels' wait on a tensor-core

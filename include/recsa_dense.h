@@ -140,6 +140,10 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
  *                  tokens appended there start from 0 in recsa_accumulate_weights.  Beside
  *                  another cache, slots past the kept ones are left as they are: a buffer that
  *                  holds an earlier cache's weights is cleared by the caller before this call.
+ * The call takes no workspace: a length outside [0, tree->length] (clamped), and a row that
+ * moves from or to a page outside the pool, are flagged in the library's own error word, which
+ * recsa_check_device_errors reads and clears with any workspace.  A row from such a page
+ * arrives as zeros; a row to such a page is not written.
  * Needs keep >= 1 and sinks + recent <= keep. */
 RECSA_API recsa_status recsa_evict(const recsa_params *params, recsa_tree *tree, const float *weights, int32_t keep,
                                    int32_t sinks, int32_t recent, int32_t *kept, recsa_tree *into,
