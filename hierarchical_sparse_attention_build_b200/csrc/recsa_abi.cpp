@@ -194,10 +194,11 @@ recsa_status build_range(const TreeGeom &g, const recsa_tree &t, int64_t length,
 // short prefill chunk), or when the sequences have their own lengths, one launch appends
 // and walks the ancestor path, a CTA per (sequence, head); otherwise the tokens are copied
 // and each level is rebuilt by its own launch, wide over the level's nodes.
+// `err`, if given, is flagged for sequences without room and new tokens on pages outside the pool.
 constexpr int64_t kPathNodes = 4;
 constexpr int kPathTokens = 64;
 recsa_status extend_tree(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t L,
-                         int chunk, void *stream) {
+                         int chunk, void *stream, uint32_t *err) {
   const int64_t L2 = L + chunk;
   const int T_new = levels_for(L2, g.b);
   const int T_old = levels_for(L, g.b);
@@ -205,10 +206,10 @@ recsa_status extend_tree(const TreeGeom &g, const recsa_tree &t, const void *k_n
   for (int l = 1; l <= T_new; ++l)
     most = std::max(most, ceil_div(L2, g.span[l]) - (l <= T_old ? L / g.span[l] : 0));
   if (t.seq_len || (chunk <= kPathTokens && most <= kPathNodes)) {
-    const int rc = launch_extend(g, t, k_new, v_new, L, chunk, T_new, stream);
+    const int rc = launch_extend(g, t, k_new, v_new, L, chunk, T_new, stream, err, err);
     return rc != 0 ? cuda_fail(rc, "append and path update") : RECSA_OK;
   }
-  const int rc = launch_append(g, t, k_new, v_new, L, chunk, stream);
+  const int rc = launch_append(g, t, k_new, v_new, L, chunk, stream, err);
   if (rc != 0) return cuda_fail(rc, "append");
   return build_range(g, t, L2, L, true, stream);
 }

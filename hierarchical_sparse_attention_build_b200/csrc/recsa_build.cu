@@ -344,6 +344,7 @@ struct ExtendArgs {
   const int32_t *pages;         // paged token cache: the page table (NULL: contiguous)
   int32_t page_shift, num_pages;
   uint32_t *err;                // optional error word: a sequence without room is flagged
+  uint32_t *page_err = nullptr;  // the same for a new token on a page outside the pool
   int64_t capacity;
   int64_t at;                   // first new slot (the length before the append; the longest one)
   int32_t chunk, hkv, b, levels;  // levels = T(at + chunk)
@@ -508,7 +509,10 @@ __global__ void __launch_bounds__(kExtendThreads, 1) extend_kernel(const ExtendA
     for (int64_t e = tid; e < (int64_t)a.chunk * 16; e += kExtendDimThreads) {  // 16 pieces a row
       const int64_t src = ((s * a.chunk + (e >> 4)) * a.hkv + h) * 16 + (e & 15);
       const int64_t row = tok_row(at + (e >> 4));
-      if (row < 0) continue;
+      if (row < 0) {
+        if (a.page_err) atomicOr(a.page_err, kErrIndex);
+        continue;
+      }
       const int64_t dst = (tok_base + row * kD) / 8 + (e & 15);  // in 16-byte pieces
       reinterpret_cast<uint4 *>(a.k_tok)[dst] = __ldg(a.k_new + src);
       reinterpret_cast<uint4 *>(a.v_tok)[dst] = __ldg(a.v_new + src);
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1) extend_kernel(const ExtendA
 // pages[b][(at + i) / page_size]; a page outside the pool is skipped.
 __global__ void append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, uint16_t *k_tok,
                               uint16_t *v_tok, int64_t capacity, int64_t at, int chunk, int hkv, int64_t rows,
-                              const int32_t *pages, int page_shift, int num_pages) {
+                              const int32_t *pages, int page_shift, int num_pages, uint32_t *page_err) {
   const int64_t n16 = rows * 16;  // 16-byte pieces
   for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n16; e += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = e >> 4;
@@ -654,7 +658,10 @@ __global__ void append_kernel(const uint4 *__restrict__ k_new, const uint4 *__re
     if (pages) {
       const int64_t t = at + i;
       const int pg = __ldg(pages + bi * (capacity >> page_shift) + (t >> page_shift));
-      if ((unsigned)pg >= (unsigned)num_pages) continue;
+      if ((unsigned)pg >= (unsigned)num_pages) {
+        if (page_err) atomicOr(page_err, kErrIndex);
+        continue;
+      }
       dst = ((((int64_t)pg * hkv + h) << page_shift) + (t & ((int64_t(1) << page_shift) - 1))) * kD + part * 8;
     } else {
       dst = ((bi * hkv + h) * capacity + at + i) * kD + part * 8;
@@ -776,9 +783,10 @@ int launch_build_level(const TreeGeom &g, const recsa_tree &t, int level, int64_
 }
 
 int launch_extend(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t at,
-                  int chunk, int levels, void *stream, uint32_t *err) {
+                  int chunk, int levels, void *stream, uint32_t *err, uint32_t *page_err) {
   ExtendArgs a;
   a.err = err;
+  a.page_err = page_err;
   a.k_new = reinterpret_cast<const uint4 *>(k_new);
   a.v_new = reinterpret_cast<const uint4 *>(v_new);
   a.k_tok = reinterpret_cast<uint16_t *>(t.k_tok);
@@ -823,7 +831,7 @@ int launch_advance_lengths(int64_t *seq_len, int batch, int64_t count, int64_t l
 }
 
 int launch_append(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t at,
-                  int chunk, void *stream) {
+                  int chunk, void *stream, uint32_t *page_err) {
   const int64_t rows = (int64_t)g.batch * chunk * g.hkv;
   const int64_t n16 = rows * 16;
   const int threads = 256;
@@ -831,7 +839,7 @@ int launch_append(const TreeGeom &g, const recsa_tree &t, const void *k_new, con
   append_kernel<<<(unsigned)grid, threads, 0, (cudaStream_t)stream>>>(
       reinterpret_cast<const uint4 *>(k_new), reinterpret_cast<const uint4 *>(v_new),
       reinterpret_cast<uint16_t *>(t.k_tok), reinterpret_cast<uint16_t *>(t.v_tok), g.capacity, at, chunk, g.hkv,
-      rows, t.page_table, t.page_table ? __builtin_ctz((unsigned)t.page_size) : 0, t.page_table ? t.num_pages : 0);
+      rows, t.page_table, t.page_table ? __builtin_ctz((unsigned)t.page_size) : 0, t.page_table ? t.num_pages : 0, page_err);
   return (int)cudaGetLastError();
 }
 

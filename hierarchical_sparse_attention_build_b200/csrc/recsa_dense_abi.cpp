@@ -209,7 +209,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
   if (s != RECSA_OK) return s;
   int rc;
   if (has_tree(tree)) {
-    s = extend_tree(g, *tree, k_new, v_new, L, chunk, stream);
+    s = extend_tree(g, *tree, k_new, v_new, L, chunk, stream, &a.hdr->err);
     if (s != RECSA_OK) return s;
   } else {
     rc = launch_append_tokens(a, tree->k_tok, tree->v_tok, k_new, v_new, L, chunk, L2, stream);
@@ -246,7 +246,8 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
   const DenseArgs a = dense_args(params, tree, view, q, 1, cap, false, false, ws);
   s = check_rows(a);
   if (s != RECSA_OK) return s;
-  int rc = has_tree(tree) ? launch_extend(g, *tree, k_new, v_new, cap - 1, 1, levels_for(cap, g.b), stream, &a.hdr->err)
+  uint32_t *const err = &a.hdr->err;
+  int rc = has_tree(tree) ? launch_extend(g, *tree, k_new, v_new, cap - 1, 1, levels_for(cap, g.b), stream, err, err)
                           : launch_append_tokens(a, tree->k_tok, tree->v_tok, k_new, v_new, 0, 1, cap, stream);
   if (rc != 0) return cuda_fail(rc, "append");
   rc = launch_advance_lengths(tree->seq_len, tree->batch, 1, cap, stream);

@@ -58,7 +58,7 @@ recsa_status check_tree(const recsa_params *p, const recsa_tree *t, TreeGeom *g,
 recsa_status build_range(const TreeGeom &g, const recsa_tree &t, int64_t length, int64_t old_length, bool extension,
                          void *stream);
 recsa_status extend_tree(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t L,
-                         int chunk, void *stream);
+                         int chunk, void *stream, uint32_t *err = nullptr);
 
 // Launchers (return cudaError_t as int; 0 = success)
 int launch_rope_table(void *ws, int rows, double base, void *stream);
@@ -70,12 +70,13 @@ int read_evict_errors(uint32_t *bits);
 int launch_build_level(const TreeGeom &g, const recsa_tree &t, int level, int64_t length, int64_t j0, int64_t j1,
                        void *stream);
 int launch_append(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t at,
-                  int chunk, void *stream);
+                  int chunk, void *stream, uint32_t *page_err = nullptr);
 // Append `chunk` tokens at slot `at` (at t.seq_len[s] when the tree has per-sequence lengths)
 // and rebuild the nodes over them, all levels in one launch (a CTA per (sequence, head)
-// walks up the levels).  levels = T of the longest new length.
+// walks up the levels).  levels = T of the longest new length.  err: a sequence without room is
+// flagged; page_err: a new token on a page outside the pool is.
 int launch_extend(const TreeGeom &g, const recsa_tree &t, const void *k_new, const void *v_new, int64_t at,
-                  int chunk, int levels, void *stream, uint32_t *err = nullptr);
+                  int chunk, int levels, void *stream, uint32_t *err = nullptr, uint32_t *page_err = nullptr);
 // seq_len[s] += count for every sequence whose new length stays within `limit` (queued after
 // the kernels that read the old lengths).
 int launch_advance_lengths(int64_t *seq_len, int batch, int64_t count, int64_t limit, void *stream);

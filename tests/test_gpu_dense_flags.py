@@ -110,3 +110,49 @@ def test_a_clean_eviction_flags_nothing():
     kept = torch.empty(2, 2, 30, dtype=torch.int32, device="cuda")
     R.evict(c.p, c.cache, torch.rand(2, 2, c.cap, device="cuda"), 30, kept)
     R.check_device_errors(c.ws)
+
+
+@pytest.mark.parametrize("with_tree", [False, True])
+@pytest.mark.parametrize("bad", [55, -4, 999])
+def test_prefill_flags_lengths_out_of_range(with_tree, bad):
+    """A length the cache's bound excludes - one that the advanced bound would admit, too - gets no
+    tokens and is flagged, with a tree over the cache and without."""
+    B, H, G, L, n = 2, 1, 4, 50, 12
+    c = Case(B, H, G, L, n, seed=11, lens=[50, 33], spare=20, garbage=0.0)
+    cache = c.cache
+    if with_tree:
+        cache = R.RecsaTree(c.p, c.cache.k_tok, c.cache.v_tok, torch.eye(128).cuda(), L, seq_len=c.cache.seq_len)
+        R.build_tree(c.p, cache)
+    cache.seq_len[0] = bad
+    before = cache.k_tok.clone()
+    new = [torch.randn(B, n, h, 128).bfloat16().cuda() for h in (H, H)]
+    out = torch.empty(B, n, H * G, 128, device="cuda")
+    R.dense_prefill_chunk(c.p, cache, *new, c.qd, out, c.ws, R.View(causal=True, own_token=True))
+    flagged(c.ws)
+    assert cache.seq_len.tolist() == [bad, 33 + n] and cache.length == L + n
+    assert torch.equal(cache.k_tok[0], before[0])
+    c.k[1, :, 33:45], c.v[1, :, 33:45] = (x[1].transpose(0, 1).cpu() for x in new)
+    c.lens = [62, 45]
+    check(out[1:], c.want(causal=True, own=True)[1:], True, c.bound())
+
+
+@pytest.mark.parametrize("with_tree,uneven,n", [(False, False, 3), (True, False, 3), (True, False, 100), (True, True, 3)])
+def test_prefill_flags_a_missing_page_that_no_query_reads(with_tree, uneven, n):
+    """The chunk's last token alone lies on the missing page, and without its own token no query
+    sees it: the append flags it."""
+    page, L = 16, 160 - n + 1
+    c = Case(1, 1, 4, L, n, seed=12, page=page, lens=[L] if uneven else None, spare=n + 8, garbage=0.0)
+    cache = c.cache
+    if with_tree:
+        cache = R.RecsaTree(c.p, c.cache.k_tok, c.cache.v_tok, torch.eye(128).cuda(), L, seq_len=c.cache.seq_len,
+                            page_table=c.table)
+        R.build_tree(c.p, cache)
+    R.check_device_errors(c.ws)
+    c.table[0, 10] = 10_000
+    new = [torch.randn(1, n, 1, 128).bfloat16().cuda() for _ in range(2)]
+    out = torch.empty(1, n, 4, 128, device="cuda")
+    R.dense_prefill_chunk(c.p, cache, *new, c.qd, out, c.ws)
+    flagged(c.ws)
+    c.k[0, 0, L:L + n], c.v[0, 0, L:L + n] = new[0][0, :, 0].cpu(), new[1][0, :, 0].cpu()
+    c.lens = [L + n]
+    check(out, c.want(causal=True), True, c.bound())
