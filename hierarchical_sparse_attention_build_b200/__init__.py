@@ -367,11 +367,14 @@ def dense_workspace_size(p: Params, batch: int, capacity: int) -> int:
 
 class DenseWorkspace:
     """Workspace of the dense operators on caches of `batch` sequences of up to `capacity`
-    tokens.  Every call writes it: one per stream (or captured graph) that may overlap."""
+    tokens.  Every call writes it: one per stream (or captured graph) that may overlap.  A
+    buffer may be larger than dense_workspace_size(); nbytes is what it holds."""
 
     def __init__(self, p: Params, batch: int, capacity: int, device, stream=None, buffer: torch.Tensor | None = None):
         self.nbytes = dense_workspace_size(p, batch, capacity)
         self.buf = buffer if buffer is not None else torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        if buffer is not None:
+            self.nbytes = buffer.numel() * buffer.element_size()
         if not self.buf.is_cuda:
             raise RecsaError(1, "the workspace is not on a CUDA device")
         _on_current_device(self.buf)

@@ -276,7 +276,7 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
   float *lse = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kDenseLse);
   const int rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, (int64_t)(ws_bytes - kDenseImages), stream);
   if (rc == kNoRoom)
-    return fail(RECSA_ERR_UNSUPPORTED, "the rotated keys of a sequence of %lld tokens do not fit a workspace",
+    return fail(RECSA_ERR_UNSUPPORTED, "the partial sums of a sequence of %lld tokens do not fit a workspace",
                 (long long)tree->length);
   return rc != 0 ? cuda_fail(rc, "attention weights") : RECSA_OK;
 }

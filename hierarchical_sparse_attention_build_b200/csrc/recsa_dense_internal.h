@@ -67,8 +67,8 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
 constexpr int kNoRoom = -1000;
 int launch_dense_chunk(const DenseArgs &a, int64_t max_keys, int64_t image_bytes, void *stream);
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream);
-// Weights per slot; `lse` has room for kMaxDenseLse floats; kNoRoom, with nothing launched, where
-// one head's rotated keys do not fit `room` bytes of images.
+// Weights per slot; `lse` has room for kMaxDenseLse floats, the images `room` bytes; kNoRoom, with
+// nothing launched, where a head's partial sums do not fit theirs.
 int launch_dense_weights(const DenseArgs &a, float *lse, float *weights, int accumulate, int64_t room, void *stream);
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,
                          int count, int64_t limit, void *stream);

@@ -35,11 +35,12 @@ struct ScoreArgs {
   DenseArgs d;
   int bh0, heads;              // the launch's (sequence, KV head) pairs
   int row0, row_tiles;         // and the query rows of each: from row0 on, in tiles of 128
-  int key_tiles;               // of a head, 128 keys
-  int nsplit;
+  int key0, key_tiles;         // the launch's key tiles of a head, 128 keys
+  int nsplit;                  // blocks a head's key tiles are shared among
+  int part0, parts;            // this launch's first of all blocks that a head's keys have in turn
   unsigned char *key_images, *query_images;  // [heads][key_tiles], [heads][row_tiles]: two parts each
   uint4 *live;                 // a key tile's tokens that were loaded
-  float2 *sums;                // [heads][row_tiles][2 nsplit][128]: a row's (maximum, sum) in part of the keys
+  float2 *sums;                // [heads][row_tiles][2 parts][128]: a row's (maximum, sum) in part of the keys
   float *weights;
   int accumulate;
 };
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(Sco
   }
   const int hl = blockIdx.x / a.key_tiles, kt = blockIdx.x % a.key_tiles;
   const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
-  const int len = dense_length(d, b, false), T = kt * kTile;
+  const int len = dense_length(d, b, false), T = (a.key0 + kt) * kTile;
   if (T >= len) return;
   unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kPartBytes;
   uint32_t word[4] = {0u, 0u, 0u, 0u};
@@ -175,13 +176,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   const int hl = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
   const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
   const int len = dense_length(d, b, PASS == 1 && tid == 0 && h == 0 && split == 0);
-  const int tiles = (len + kTile - 1) / kTile;
+  const int tiles = min(a.key_tiles, max(0, (len + kTile - 1) / kTile - a.key0));
   const int kt0 = (int)((int64_t)tiles * split / a.nsplit), kt1 = (int)((int64_t)tiles * (split + 1) / a.nsplit);
   if (kt0 >= kt1) {  // pass 2 reads every block's sums
     if (PASS == 1)
       for (int e = tid; e < a.row_tiles * 2 * kTile; e += kScoreThreads) {
         const int rt = e / (2 * kTile), set = e / kTile % 2;
-        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) + split * 2 + set) * kTile + e % kTile] =
+        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.parts) + (a.part0 + split) * 2 + set) * kTile + e % kTile] =
             make_float2(-INFINITY, 0.f);
       }
     return;
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   auto last_tile = [&](int rt) {
     const int row = min(a.row0 + (rt + 1) * kTile, d.nq << d.group_shift) - 1;
     const int p = row_position(d, len, row);
-    return max(kt0 + 1, min(kt1, (max(p, 0) + kTile - 1) / kTile));
+    return max(kt0 + 1, min(kt1, (max(p, 0) + kTile - 1) / kTile - a.key0));
   };
 
   if (warp < kEpilogueWarps) {
@@ -227,10 +228,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
         asm volatile("bar.sync 1, 256;" ::: "memory");  // the last row tile's values have been read
         if (tid < kTile) {
           const int p = row_position(d, len, a.row0 + rt * kTile + tid);
-          const float2 *src = a.sums + ((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) * kTile + tid;
+          const float2 *src = a.sums + ((int64_t)hl * a.row_tiles + rt) * (2 * a.parts) * kTile + tid;
           float m = -INFINITY, l = 0.f;
-          for (int j = 0; j < 2 * a.nsplit; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
-          for (int j = 0; j < 2 * a.nsplit; ++j) {
+          for (int j = 0; j < 2 * a.parts; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
+          for (int j = 0; j < 2 * a.parts; ++j) {
             const float2 v = __ldcg(src + j * kTile);
             if (v.x != -INFINITY) l += v.y * exp2_approx(v.x - m);
           }
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
       float m = -INFINITY, l = 0.f;
       for (int kt = kt0; kt < end; ++kt, ++n) {
         if ((int)(n & 1) != set) continue;
-        const int T = kt * kTile;
+        const int T = (a.key0 + kt) * kTile;
         const uint4 live = __ldg(a.live + (int64_t)hl * a.key_tiles + kt);
         wait(&sm.d_full[set], (n >> 1) & 1);
         umma::fence_after_sync();
@@ -321,13 +322,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
         }
       }
       if (PASS == 1)
-        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.nsplit) + split * 2 + set) * kTile + trow] = make_float2(m, l);
+        a.sums[(((int64_t)hl * a.row_tiles + rt) * (2 * a.parts) + (a.part0 + split) * 2 + set) * kTile + trow] =
+            make_float2(m, l);
     }
     if (PASS == 2) {
       asm volatile("bar.sync 1, 256;" ::: "memory");
       float *const w = a.weights + ((int64_t)b * d.hkv + h) * d.capacity;
-      for (int t = kt0 * kTile + tid; t < min(kt1 * kTile, len); t += kEpilogueWarps * 32) {
-        const float v = sm.acc[t - kt0 * kTile];
+      const int t0 = (a.key0 + kt0) * kTile;
+      for (int t = t0 + tid; t < min((a.key0 + kt1) * kTile, len); t += kEpilogueWarps * 32) {
+        const float v = sm.acc[t - t0];
         w[t] = a.accumulate ? w[t] + v : v;
       }
     }
@@ -448,21 +451,33 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
   ScoreArgs a = {};
   a.d = d;
   a.weights = weights;
-  a.key_tiles = (int)ceil_div(std::max(d.length, 1), kTile);
+  const int64_t key_tiles = ceil_div(std::max(d.length, 1), kTile);
+  // As many heads and rows a launch as the images' room and the sums' hold: an eighth of the room
+  // for one head's rows, at least one tile of them.  Later rows add to what earlier ones wrote.  A
+  // head whose images do not fit has its keys in slices, turned for pass 1 and again for pass 2.
+  constexpr int64_t kKeyBytes = kPartBytes + (int64_t)sizeof(uint4);
+  const int64_t sums = (int64_t)kDensePartBytes / (2 * (int64_t)(kTile * sizeof(float2)));  // of a row tile and a part
+  const int64_t all_tiles = ceil_div(rows, kTile);
+  int64_t slice = 0, slices = 0, least = 0;  // key tiles a launch; launches a pass; fewest blocks a slice
+  auto slice_for = [&](int64_t row_tiles) {
+    slice = std::min(key_tiles, (room - row_tiles * (int64_t)kPartBytes) / kKeyBytes);
+    if (slice < 1) return false;
+    slices = ceil_div(key_tiles, slice);
+    least = ceil_div(slice, kMaxRange);
+    return sums / (least * slices) >= 1;
+  };
+  if (!slice_for(1)) return kNoRoom;
+  int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, room / 8 / kPartBytes));
+  while (tiles > 1 && (!slice_for(tiles) || tiles > sums / (least * slices))) tiles = (tiles + 1) / 2;
+  slice_for(tiles);
+  const int64_t key_bytes = slice * kKeyBytes;
+  const int64_t fit = slices > 1 ? 1 : std::min(room / (key_bytes + tiles * (int64_t)kPartBytes), sums / (least * tiles));
   cudaError_t e = cudaFuncSetAttribute(dense_scores_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e != cudaSuccess) return (int)e;
   const cudaStream_t st = (cudaStream_t)stream;
   const int sms = dense_sm_count();
-  // As many heads and rows a launch as the images' room and the sums' hold: an eighth of the room
-  // for one head's rows, at least one tile of them.  Later rows add to what earlier ones wrote.
-  const int64_t key_bytes = a.key_tiles * (int64_t)(kPartBytes + sizeof(uint4)), least = ceil_div(a.key_tiles, kMaxRange);
-  const int64_t sums = (int64_t)kDensePartBytes / (2 * (int64_t)(kTile * sizeof(float2)));  // of a row tile and a part
-  const int64_t all_tiles = ceil_div(rows, kTile);
-  const int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, std::min(room / 8 / kPartBytes, sums / least)));
-  const int64_t fit = std::min(room / (key_bytes + tiles * (int64_t)kPartBytes), sums / (least * tiles));
-  if (fit < 1) return kNoRoom;
   // Both passes read a head's images for every row tile: heads in turn, as many as stay in the L2
   // cache from the turning to the last reading (64 queries over 8 x 32768 tokens, whose images are
   // 134 MB: 167 -> 161 us).
@@ -471,7 +486,7 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
     a.bh0 = (int)bh0;
     a.heads = (int)std::min(step, heads - bh0);
     a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
-    a.query_images = a.key_images + (int64_t)a.heads * a.key_tiles * kPartBytes;
+    a.query_images = a.key_images + (int64_t)a.heads * slice * kPartBytes;
     a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * tiles * kPartBytes);
     a.sums = reinterpret_cast<float2 *>(reinterpret_cast<char *>(d.hdr) + kDensePart);
     for (int64_t rt0 = 0; rt0 < all_tiles; rt0 += tiles) {
@@ -480,13 +495,26 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
       a.accumulate = accumulate || rt0 > 0;
       // one wave of blocks where that leaves each at most kMaxRange key tiles
       a.nsplit = (int)std::min<int64_t>(
-          {std::max<int64_t>(least, sms / a.heads), a.key_tiles, sums / ((int64_t)a.heads * a.row_tiles)});
-      const int64_t blocks = (int64_t)a.heads * (a.key_tiles + (int64_t)a.row_tiles * (kTile / kTurnRows));
-      dense_score_images_kernel<<<(unsigned)blocks, kTurnThreads, 0, st>>>(a);
-      dense_scores_kernel<1><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
-      dense_scores_kernel<2><<<(unsigned)(a.heads * a.nsplit), kScoreThreads, kScoreSmem, st>>>(a);
-      e = cudaGetLastError();
-      if (e != cudaSuccess) return (int)e;
+          {std::max<int64_t>(least, sms / a.heads), slice, sums / ((int64_t)a.heads * a.row_tiles * slices)});
+      a.parts = (int)(a.nsplit * slices);
+      for (int pass = 1; pass <= 2; ++pass) {
+        for (int64_t i = 0; i < slices; ++i) {
+          a.key0 = (int)(i * slice);
+          a.key_tiles = (int)std::min(slice, key_tiles - i * slice);
+          a.part0 = (int)(i * a.nsplit);
+          // the queries once; the keys once a pass, or once where one slice holds them all
+          const int64_t turned = i > 0 || pass > 1 ? 0 : (int64_t)a.row_tiles * (kTile / kTurnRows);
+          if (pass == 1 || slices > 1)
+            dense_score_images_kernel<<<(unsigned)(a.heads * (a.key_tiles + turned)), kTurnThreads, 0, st>>>(a);
+          const unsigned blocks = (unsigned)(a.heads * a.nsplit);
+          if (pass == 1)
+            dense_scores_kernel<1><<<blocks, kScoreThreads, kScoreSmem, st>>>(a);
+          else
+            dense_scores_kernel<2><<<blocks, kScoreThreads, kScoreSmem, st>>>(a);
+          e = cudaGetLastError();
+          if (e != cudaSuccess) return (int)e;
+        }
+      }
     }
   }
   return 0;

@@ -114,7 +114,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
  *   weights : fp32 [batch][Hkv][capacity]; slots [0, L) are overwritten (accumulate = 0) or
  *             added to (accumulate = 1), slots at or past a sequence's L are left as they are.
  * Views with a window are RECSA_ERR_UNSUPPORTED, and so are more than 8 query rows a KV group
- * over sequences of more than about 2.5 million tokens (their rotated keys do not fit). */
+ * over sequences of more than about 100 million tokens (their partial sums do not fit). */
 RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, const recsa_tree *tree,
                                                 const recsa_view *view, const void *q, int32_t num_queries,
                                                 float *weights, int32_t accumulate, void *ws, size_t ws_bytes,
