@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     const int span = (T / kSpan) * 2 + (sink ? 1 : 0);
     if (span != turned) {
       turned = span;
-      turn_queries<NR>(a, sm.q[sink], (sink ? base_sink : p_max - a.back) - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
+      turn_queries<NR>(a, sm.q[sink], (sink ? base_sink : p_max) - a.back - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
     }
     cp_async_wait<1>();
     __syncwarp();

@@ -51,9 +51,9 @@ __device__ __forceinline__ int dense_length(const DenseArgs &a, int b, bool repo
 __device__ __forceinline__ int dense_position(const DenseArgs &a, int len, int i) {
   return a.causal ? len - a.nq + i + a.own : len;
 }
-// Where a query of bound p sits for the sinks (those outside its window).
+// The bound that a query of bound p has for the sinks (those outside its window).
 __device__ __forceinline__ int sink_position(const DenseArgs &a, int p) {
-  return (a.rank_sinks ? min(p, a.sinks + a.window) : p) - a.back;
+  return a.rank_sinks ? min(p, a.sinks + a.window) : p;
 }
 // The tokens a query at p sees, besides the first min(sinks, p): [first, p).
 __device__ __forceinline__ int window_first(const DenseArgs &a, int p) {

@@ -192,7 +192,7 @@ __device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *
   constexpr int kPer = kQueryRows / 16;  // rows r0 + 16 i of a thread
   auto position = [&](int i) {
     const int p = dense_position(d, it.len, it.q0 + ((r0 + 16 * i) >> gs));
-    return sink ? sink_position(d, p) : p - d.back;
+    return sink ? sink_position(d, p) : p;
   };
   uint4 lo[kPer], hi[kPer];
 #pragma unroll
@@ -213,7 +213,7 @@ __device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *
 #pragma unroll
   for (int i = 2; i < kPer; ++i) even = even && position(i) == p0 + i * by;
   Turn t, step;
-  t.set(f, p0);
+  t.set(f, p0 - d.back);
   if (by != 0) step.set(f, by);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void turn_queries(const ChunkArgs &a, unsigned char *
     put_row(q + (row >> 7) * kTileBytes, row & 127, ch, ol, oh);
     if (i + 1 < kPer) {
       if (!even)
-        t.set(f, position(i + 1));
+        t.set(f, position(i + 1) - d.back);
       else if (by != 0)
         t.advance(step);
     }
