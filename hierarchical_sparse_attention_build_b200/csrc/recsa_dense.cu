@@ -20,6 +20,10 @@ constexpr int kOStride = kD + 8;              // floats of an output row in shar
 constexpr int kDealtSequences = kThreads;     // sequences whose steps can be dealt out (a thread counts one's)
 constexpr int kDealtSteps = 16;               // steps a block is worth starting for
 constexpr float kRowsRescale = 64.f;          // a row's maximum may lag by 2^64 before its output is rescaled
+// A row whose output overflows that way (values above 2^63, infinities) is computed once more by
+// careful_row, with weights of at most 2^-32: sums of 2^30 of them stay finite.
+constexpr float kRowsLarge = 0x1p96f;         // outputs up to here join without overflow
+constexpr float kRowsLift = 32.f;
 
 template <int R>  // query rows of a tile: queries x heads of a KV group
 struct RowsSmem {
@@ -32,6 +36,7 @@ struct RowsSmem {
   float m[kWarps][R], l[kWarps][R];
   int pos[R];                          // a row's position; 0 or less: nothing visible
   int last;
+  int range[2];                        // the block's steps of the tile
   int dealt[kDealtSequences + 1];      // steps before each sequence, when steps are dealt out to the blocks
 };
 
@@ -243,6 +248,77 @@ struct Dealt {
   }
 };
 
+// One row over the steps [begin, stop) of its tile by one warp, in fp32: dimensions 4 lane .. 4 lane
+// + 3 of the weighted sum of values, the weights' sum and the maximum they are relative to.  Every
+// value is weighed by itself: one that the row does not see is not touched, and an infinity does
+// not meet the zero that a weight's second part may be.
+template <int R>
+__device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg, int row, int b, int h, int p_max,
+                            int base_sink, float (&acc)[4], float &m, float &sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = sm.pos[row];
+  float *const turned = reinterpret_cast<float *>(sm.ang[warp]);
+  const uint64_t *f = ws_freq(a.hdr);
+  float top = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int st = sm.range[0]; st < sm.range[1]; ++st) {
+    const bool sink = rg.sink(st);
+    const int T = rg.token(st), delta = (sink ? base_sink : p_max) - a.back - (T & ~(kSpan - 1));
+    __syncwarp();
+#pragma unroll
+    for (int i = lane; i < kHalf; i += 32) {  // the row turned to the span, as the keys' table is
+      const float2 w = rotation(delta, __ldg(f + i));
+      const float x = sm.q[sink][row][i], y = sm.q[sink][row][i + kHalf];
+      turned[i] = x * w.x - y * w.y;
+      turned[i + kHalf] = y * w.x + x * w.y;
+    }
+    __syncwarp();
+    // two lanes a key, half of the dimensions each
+    const int t = T + (lane & 15);
+    const bool in = sink ? t < min(p, rg.hi1) : t >= window_first(a, p) && t < p;
+    const int64_t r = in ? cache_row(a, b, h, t) : -1;
+    float s = 0.f;
+    if (r >= 0) {
+      const uint32_t *key = reinterpret_cast<const uint32_t *>(a.k + r * kD);
+      const unsigned char *tr = sm.table + (t & (kSpan - 1)) * kTableStride;
+#pragma unroll 4
+      for (int i = (lane >> 4) * 16; i < (lane >> 4) * 16 + 16; ++i) {
+        const float4 w = *reinterpret_cast<const float4 *>(tr + ((i ^ ((t & 1) << 2)) << 4));
+        const uint32_t x = __ldg(key + i), y = __ldg(key + i + 32);
+        s += turned[2 * i] * (bf16_lo(x) * w.x - bf16_lo(y) * w.z) + turned[2 * i + 1] * (bf16_hi(x) * w.y - bf16_hi(y) * w.w);
+        s += turned[2 * i + kHalf] * (bf16_lo(y) * w.x + bf16_lo(x) * w.z) +
+             turned[2 * i + 1 + kHalf] * (bf16_hi(y) * w.y + bf16_hi(x) * w.w);
+      }
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (r < 0) s = -INFINITY;
+    float x = s;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    if (x > top) {
+      const float w = top == -INFINITY ? 0.f : exp2_approx(top - x);
+      top = x;
+      sum *= w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= w;
+    }
+    const float weight = exp2_approx(s - ((top == -INFINITY ? 0.f : top) + kRowsLift));
+    const uint32_t seen = __ballot_sync(0xffffffffu, r >= 0);
+#pragma unroll 4
+    for (int key = 0; key < kStep; ++key) {
+      const float w = __shfl_sync(0xffffffffu, weight, key);
+      const int64_t v_row = __shfl_sync(0xffffffffu, r, key);
+      if (!((seen >> key) & 1u)) continue;
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(a.v + v_row * kD) + lane);
+      sum += w;
+      acc[0] += w * bf16_lo(v.x), acc[1] += w * bf16_hi(v.x), acc[2] += w * bf16_lo(v.y), acc[3] += w * bf16_hi(v.y);
+    }
+  }
+  m = top == -INFINITY ? top : top + kRowsLift;
+}
+
 // One tile of 8 NR query rows (queries x heads of a KV group) against one block's share of the keys
 // they see.  Each warp walks its own steps of 16 keys with an online softmax, its keys and values
 // fetched one step ahead with cp.async into memory of its own, so warps never wait for one another
@@ -342,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     begin = (int)((int64_t)rg.total * split / a.nsplit);
     stop = (int)((int64_t)rg.total * (split + 1) / a.nsplit);
   }
+  if (PV && tid == 0) sm.range[0] = begin, sm.range[1] = stop;
   // this warp's steps; the first loads are on their way while the query rows are turned
   const int st0 = begin + (int)((int64_t)(stop - begin) * warp / kWarps),
             st1 = begin + (int)((int64_t)(stop - begin) * (warp + 1) / kWarps);
@@ -396,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
 
   // this thread's query rows: nt * 8 + 2 c + i
   float m[NR][2], l[NR][2], o[PV ? NR : 1][8][4];
-  int p_lo = 0x7fffffff, p_hi = 0;  // the least and largest position of the tile's rows
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
@@ -409,8 +485,6 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       for (int d = 0; d < 8; ++d) o[nt][d][0] = o[nt][d][1] = o[nt][d][2] = o[nt][d][3] = 0.f;
     }
   }
-  p_lo = p_min;
-  p_hi = p_max;
   uint32_t qh[NR][16], ql[NR][16];
   int turned = -1;  // the span the query rows are turned for (sinks: odd)
 
@@ -438,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       cp_async_commit();
     }
     // every row sees every key of the step unless it meets an end of some row's range
-    const bool whole = live == 0xffffu && (sink ? T + kStep <= min(p_lo, rg.hi1)
-                                                : T + kStep <= p_lo && T >= window_first(a, p_hi));
+    const bool whole = live == 0xffffu && (sink ? T + kStep <= min(p_min, rg.hi1)
+                                                : T + kStep <= p_min && T >= window_first(a, p_max));
     bool seen[NR][4];
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
@@ -462,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       *reinterpret_cast<float2 *>(dst + 8 * a.score_stride) = make_float2(s[0][2], s[0][3]);
     }
     // Weights from the maximum so far: weights, sums and outputs hold numbers up to 2^127 with
-    // the same relative precision.  Only a row whose maximum has grown by more than 2^64 (or that
-    // has none yet) takes a new one.
+    // the same relative precision (a row's output beyond kRowsLarge is computed again below).  Only
+    // a row whose maximum has grown by more than 2^64 (or that has none yet) takes a new one.
     bool up = false;
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
@@ -624,6 +698,27 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
         for (int i = 0; i < kPer; i += 4) {
           const float4 u = *reinterpret_cast<const float4 *>(wo + (w * R + row) * kOStride + d0 + i);
           acc[i] += f * u.x, acc[i + 1] += f * u.y, acc[i + 2] += f * u.z, acc[i + 3] += f * u.w;
+        }
+      }
+    }
+  }
+  if (PV) {  // (a row's threads are lanes of one warp)
+    float size = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) size += fabsf(acc[i]);
+    const uint32_t large = __ballot_sync(0xffffffffu, !(size <= kRowsLarge));
+    if (large) {
+#pragma unroll 1
+      for (int j = 0; j < NR; ++j) {
+        if (!(large >> (j * (32 / NR)) << (32 - 32 / NR))) continue;
+        float x[4], xm, xsum;
+        careful_row<R>(a, sm, rg, warp * NR + j, b, h, p_max, base_sink, x, xm, xsum);
+        const bool mine = row == warp * NR + j;
+        if (mine) mx = xm, sum = xsum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float y = __shfl_sync(0xffffffffu, x[i & 3], (d0 + i) / 4);
+          if (mine) acc[i] = y;
         }
       }
     }
