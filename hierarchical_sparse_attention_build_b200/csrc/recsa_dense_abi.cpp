@@ -52,6 +52,27 @@ recsa_status check_dense_ws(const recsa_params *p, const recsa_tree *t, const vo
   return RECSA_OK;
 }
 
+// Buffers that one call reads in some blocks and writes in others may not overlap.
+struct Extent {
+  const void *p;
+  size_t bytes;
+  const char *name;
+};
+recsa_status check_apart(const Extent &a, const Extent &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (a.p && b.p && x < y + b.bytes && y < x + a.bytes)
+    return fail(RECSA_ERR_INVALID_ARGUMENT, "%s overlaps %s", a.name, b.name);
+  return RECSA_OK;
+}
+size_t query_bytes(const recsa_params *p, const recsa_tree *t, int32_t nq) {
+  return (size_t)t->batch * nq * p->num_q_heads * kRowBytes;
+}
+recsa_status check_out(const recsa_params *p, const recsa_tree *t, const void *q, int32_t nq, const void *out,
+                       int32_t out_is_fp32) {
+  const size_t bytes = query_bytes(p, t, nq);
+  return check_apart({out, bytes * (out_is_fp32 ? 2 : 1), "out"}, {q, bytes, "q"});
+}
+
 DenseArgs dense_args(const recsa_params *p, const recsa_tree *t, const recsa_view *v, const void *q, int32_t nq,
                      int64_t length, bool causal, bool own, void *ws) {
   DenseArgs a = {};
@@ -179,6 +200,7 @@ RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recs
   const DenseArgs a = dense_args(params, tree, view, q, num_queries, tree->length, view && view->causal,
                                  view && view->own_token, ws);
   s = check_rows(a);
+  if (s == RECSA_OK) s = check_out(params, tree, q, num_queries, out, out_is_fp32);
   if (s != RECSA_OK) return s;
   return attend(a, view, out, out_is_fp32, ws_bytes, stream);
 }
@@ -206,6 +228,7 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
   if (s != RECSA_OK) return s;
   const DenseArgs a = dense_args(params, tree, view, q, chunk, L2, true, view && view->own_token, ws);
   s = check_rows(a);
+  if (s == RECSA_OK) s = check_out(params, tree, q, chunk, out, out_is_fp32);
   if (s != RECSA_OK) return s;
   int rc;
   if (has_tree(tree)) {
@@ -245,6 +268,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
   const int64_t cap = tree->capacity;
   const DenseArgs a = dense_args(params, tree, view, q, 1, cap, false, false, ws);
   s = check_rows(a);
+  if (s == RECSA_OK) s = check_out(params, tree, q, 1, out, out_is_fp32);
   if (s != RECSA_OK) return s;
   uint32_t *const err = &a.hdr->err;
   int rc = has_tree(tree) ? launch_extend(g, *tree, k_new, v_new, cap - 1, 1, levels_for(cap, g.b), stream, err, err)
@@ -272,6 +296,9 @@ RECSA_API recsa_status recsa_accumulate_weights(const recsa_params *params, cons
   const DenseArgs a = dense_args(params, tree, view, q, num_queries, tree->length, view && view->causal,
                                  view && view->own_token, ws);
   s = check_rows(a);
+  if (s == RECSA_OK)
+    s = check_apart({weights, (size_t)tree->batch * params->num_kv_heads * tree->capacity * sizeof(float), "weights"},
+                    {q, query_bytes(params, tree, num_queries), "q"});
   if (s != RECSA_OK) return s;
   float *lse = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kDenseLse);
   const int rc = launch_dense_weights(a, lse, weights, accumulate ? 1 : 0, (int64_t)(ws_bytes - kDenseImages), stream);
@@ -327,6 +354,23 @@ RECSA_API recsa_status recsa_evict(const recsa_params *params, recsa_tree *tree,
         into->v_tok == tree->k_tok)
       return fail(RECSA_ERR_INVALID_ARGUMENT, "into shares its rows with tree (pass NULL to compact in place)");
   }
+  // Rows that are read and written.  (The pages of two pools may interleave without sharing a row:
+  // what a page table names is the caller's.)
+  const size_t slots = (size_t)tree->batch * params->num_kv_heads;
+  const Extent from[2] = {{tree->k_tok, tree->page_table ? 0 : slots * tree->capacity * kRowBytes, "tree->k_tok"},
+                          {tree->v_tok, tree->page_table ? 0 : slots * tree->capacity * kRowBytes, "tree->v_tok"}};
+  const Extent dest[2] = {{to->k_tok, to->page_table ? 0 : slots * to->capacity * kRowBytes, "into->k_tok"},
+                          {to->v_tok, to->page_table ? 0 : slots * to->capacity * kRowBytes, "into->v_tok"}};
+  if (!to->page_table) s = check_apart(dest[0], dest[1]);
+  for (int i = 0; i < 4 && s == RECSA_OK && !in_place && !tree->page_table && !to->page_table; ++i)
+    s = check_apart(dest[i & 1], from[i >> 1]);
+  const Extent old_weights = {weights, slots * tree->capacity * sizeof(float), "weights"},
+               new_weights = {into_weights, slots * to->capacity * sizeof(float), "into_weights"},
+               slots_kept = {kept, slots * keep * sizeof(int32_t), "kept"};
+  if (s == RECSA_OK && !(in_place && into_weights == weights)) s = check_apart(new_weights, old_weights);
+  if (s == RECSA_OK) s = check_apart(slots_kept, old_weights);
+  if (s == RECSA_OK) s = check_apart(slots_kept, new_weights);
+  if (s != RECSA_OK) return s;
   if (into_weights) {
     s = check_buffer(into_weights, "into_weights");
     if (s != RECSA_OK) return s;

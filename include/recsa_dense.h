@@ -10,6 +10,8 @@
  * 16-byte alignment, asynchronous calls, nothing allocated, argument errors reported with a
  * status and nothing launched, per-sequence lengths clamped and flagged, page-table entries
  * outside the pool never dereferenced (such a token is skipped and flagged).
+ * Outputs may not overlap the call's queries, weights or kept slots (refused); what the pages
+ * of one pool or another name is the caller's.
  *
  * A cache without a tree: in every call here tree->k_node, tree->v_node and tree->pooler may
  * be NULL together.  Calls that add tokens update the tree when there is one, and write the

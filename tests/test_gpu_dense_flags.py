@@ -156,3 +156,39 @@ def test_prefill_flags_a_missing_page_that_no_query_reads(with_tree, uneven, n):
     c.k[0, 0, L:L + n], c.v[0, 0, L:L + n] = new[0][0, :, 0].cpu(), new[1][0, :, 0].cpu()
     c.lens = [L + n]
     check(out, c.want(causal=True), True, c.bound())
+
+
+def test_neighbouring_buffers_are_accepted():
+    """Queries and output, weights and kept slots side by side in one allocation; two page pools
+    interleaved page by page, whose ranges overlap and whose rows do not."""
+    B, H, G, L, keep, page = 1, 2, 2, 64, 20, 16
+    c = Case(B, H, G, L, 1, seed=13)
+    want = c.attend(False)
+    both = torch.empty(2, *c.qd.shape, dtype=torch.bfloat16, device="cuda")
+    both[0] = c.qd
+    R.dense_attend(c.p, c.cache, both[0], both[1], c.ws)
+    assert torch.equal(both[1], want)
+    w = torch.rand(3, B, H, L, device="cuda")
+    kept = torch.empty(B, H, keep, dtype=torch.int32, device="cuda")
+    w0 = w[0].cpu()
+    R.evict(c.p, c.cache, w[0], keep, kept, into_weights=w[1])
+    for h in range(H):
+        idx = F.evict(w0[0, h], L, keep, 0, 0)
+        assert kept[0, h].tolist() == idx and torch.equal(w[1, 0, h, :keep].cpu(), w0[0, h, idx])
+    # pages 0, 2, 4, ... of one pool hold K, the others V
+    pool = torch.zeros(10, H, page, 128, dtype=torch.bfloat16, device="cuda")
+    k, v = pool[:9], pool[1:]
+    table = torch.tensor([[0, 4, 2, 6]], dtype=torch.int32, device="cuda")
+    d = Case(B, H, G, L, 1, seed=14)
+    for i, pg in enumerate(table[0].tolist()):
+        k[pg], v[pg] = (x[0, :, i * page:(i + 1) * page].cuda() for x in (d.k, d.v))
+    cache = R.TokenCache(d.p, k, v, L, page_table=table)
+    out = torch.empty(B, 1, H * G, 128, device="cuda")
+    R.dense_attend(d.p, cache, d.qd, out, d.ws)
+    check(out, d.want(), True, d.bound())
+    R.evict(d.p, cache, w[2], keep, kept)
+    R.check_device_errors(d.ws)
+    for h in range(H):
+        idx = F.evict(w[2, 0, h].cpu(), L, keep, 0, 0)
+        got = torch.cat([k[pg, h] for pg in (0, 4)])[:keep].cpu(), torch.cat([v[pg, h] for pg in (0, 4)])[:keep].cpu()
+        assert torch.equal(got[0], d.k[0, h, idx]) and torch.equal(got[1], d.v[0, h, idx])
