@@ -194,6 +194,7 @@ class RecsaTree:
             assert seq_len.dtype == torch.int64 and seq_len.is_contiguous() and seq_len.numel() == batch
         self.seq_len = seq_len
         self.page_table = page_table
+        self.devices = {t.device for t in (k_tok, v_tok, k_node, v_node, pooler, seq_len, page_table) if t is not None}
         self.c = Tree(batch, 0, capacity, length, k_tok.data_ptr(), v_tok.data_ptr(), k_node.data_ptr(),
                       v_node.data_ptr(), pooler.data_ptr(), seq_len.data_ptr() if seq_len is not None else None,
                       page_table.data_ptr() if page_table is not None else None, page_size, num_pages)
@@ -390,6 +391,15 @@ def _on_current_device(*tensors: torch.Tensor) -> None:
             raise RecsaError(1, f"a tensor on {t.device}, the current device is cuda:{dev}")
 
 
+def _cache_here(p: Params, tree: RecsaTree, name: str = "the cache") -> None:
+    """Every tensor of the cache is on the current device, and the cache has p's KV heads."""
+    if tree.p.num_kv_heads != p.num_kv_heads:
+        raise RecsaError(1, f"{name} has {tree.p.num_kv_heads} KV heads, params {p.num_kv_heads}")
+    dev = torch.cuda.current_device()
+    if len(tree.devices) != 1 or next(iter(tree.devices)).index != dev:
+        raise RecsaError(1, f"{name}'s tensors are on {sorted(map(str, tree.devices))}, the current device is cuda:{dev}")
+
+
 def _dense_rows(p: Params, tree: RecsaTree, t: torch.Tensor, heads: int, name: str, dtypes=(torch.bfloat16,)) -> None:
     """t is [batch][n][heads][128], contiguous, of one of the types."""
     if t.dtype not in dtypes:
@@ -408,7 +418,8 @@ def _dense_q(p: Params, tree: RecsaTree, q: torch.Tensor, out: torch.Tensor, ws:
     _dense_rows(p, tree, out, p.num_q_heads, "out", _OUT_TYPES)
     if out.shape != q.shape:
         raise RecsaError(1, f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
-    _on_current_device(tree.k_tok, q, out, ws.buf)
+    _cache_here(p, tree)
+    _on_current_device(q, out, ws.buf)
 
 
 def _dense_new(p: Params, tree: RecsaTree, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor) -> None:
@@ -469,7 +480,8 @@ def accumulate_weights(p: Params, tree: RecsaTree, q: torch.Tensor, weights: tor
     summed over queries and group heads, into weights [B][Hkv][capacity] (fp32)."""
     _dense_rows(p, tree, q, p.num_q_heads, "q")
     _weights_of(tree, weights, "weights")
-    _on_current_device(tree.k_tok, q, ws.buf)
+    _cache_here(p, tree)
+    _on_current_device(q, ws.buf)
     _check(_lib.recsa_accumulate_weights(ctypes.byref(p), ctypes.byref(tree.c), _view(view), _ptr(q), q.shape[1],
                                          _ptr(weights), int(accumulate), _ptr(ws.buf), ws.nbytes, _stream(stream)))
 
@@ -487,7 +499,10 @@ def evict(p: Params, tree: RecsaTree, weights: torch.Tensor, keep: int, kept: to
                             f"[{tree.batch}][{p.num_kv_heads}][{keep}]")
     if into_weights is not None:
         _weights_of(tree if into is None else into, into_weights, "into_weights")
-    _on_current_device(tree.k_tok, kept, *(() if into is None else (into.k_tok,)))
+    _cache_here(p, tree)
+    if into is not None:
+        _cache_here(p, into, "into")
+    _on_current_device(kept)
     _check(_lib.recsa_evict(ctypes.byref(p), ctypes.byref(tree.c), _ptr(weights), keep, sinks, recent, _ptr(kept),
                             None if into is None else ctypes.byref(into.c), _ptr(into_weights), _stream(stream)))
 
