@@ -83,10 +83,18 @@ RECSA_API recsa_status recsa_dense_workspace_init(const recsa_params *params, in
 /* Attention of num_queries queries per sequence over the tokens that are in the cache.
  *   q   : bf16 [batch][num_queries][Hq][128], pre-RoPE.
  *   out : [batch][num_queries][Hq][128], fp32 if out_is_fp32 else bf16.
- * With an fp32 output scores and probabilities keep 16 bits of each operand on the tensor
- * cores (the output is within about 1e-5 of the formula, relative).  With a bf16 output the
- * chunk kernel rounds the rotated rows to fp16 and the probabilities to bf16 (the output is
- * within about 2.5e-3, its own rounding 1.7e-3 of that). */
+ * Accuracy.  The rows kernel, and so every fp32 output, keeps two bf16 parts of rotated rows and
+ * probabilities on the tensor cores: a score is off by at most 3 * 2^-16 softmax_scale |q| |k|,
+ * an output by twice that and 2^-16 of the largest value seen.  The chunk kernel rounds rotated
+ * rows to fp16 and probabilities to bf16: 2^-10 softmax_scale |q| |k|, and 2^-8 beside the
+ * output's own rounding.  Errors so grow with the scores; measured on random rows, as shares of
+ * the output's norm (and of the worst row's):
+ *   spread of the scores        1                    5                    20
+ *   fp32 output           4e-6 (9e-6)          1.1e-5 (5e-5)        2.8e-5 (1.8e-4)
+ *   bf16, rows kernel     1.7e-3 (2.2e-3)      1.7e-3 (2.3e-3)      1.4e-3 (2.2e-3)
+ *   bf16, chunk kernel    2.4e-3 (3.6e-3)      2.4e-3 (5.0e-3)      2.4e-3 (1.2e-2)
+ * The automatic choice goes by the sizes of the whole call; view->kernel = 1 keeps a query's
+ * accuracy the same whatever it is batched with. */
 RECSA_API recsa_status recsa_dense_attend(const recsa_params *params, const recsa_tree *tree, const recsa_view *view,
                                           const void *q, int32_t num_queries, void *out, int32_t out_is_fp32,
                                           void *ws, size_t ws_bytes, recsa_stream_t stream);
@@ -113,6 +121,7 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
 
 /* The softmax weight that each cache slot receives from the queries, summed over the queries
  * and over the query heads of its KV group, in fp32.
+ * Scores are as accurate as those of an fp32 output above.
  *   weights : fp32 [batch][Hkv][capacity]; slots [0, L) are overwritten (accumulate = 0) or
  *             added to (accumulate = 1), slots at or past a sequence's L are left as they are.
  * Views with a window are RECSA_ERR_UNSUPPORTED, and so are more than 8 query rows a KV group
