@@ -943,16 +943,13 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
   const int64_t steps = all * (ceil_div(max_keys, kStep) + 2);
   if (a.seq_len && steps >= 64 * (int64_t)places && steps < (int64_t)1 << 31 && a.tiles == 1 && a.batch <= kDealtSequences && items == all && items <= kMaxShared) {
     a.nsplit = 1;
-    if (lse) return nr == 1 ? run_rows<1, 1, true>(a, items, places, lse, nullptr, 0, stream)
-                            : run_rows<2, 1, true>(a, items, places, lse, nullptr, 0, stream);
+    if (lse) return run_rows<1, 1, true>(a, items, places, lse, nullptr, 0, stream);
     return nr == 1 ? run_rows<1, 0, true>(a, items, places, nullptr, nullptr, 0, stream)
                    : run_rows<2, 0, true>(a, items, places, nullptr, nullptr, 0, stream);
   }
   a.nsplit = pick_split(items, max_keys, places, 8 * nr);
   const int64_t grid = items * a.nsplit;
-  if (lse)
-    return nr == 1 ? run_rows<1, 1>(a, items, grid, lse, nullptr, 0, stream)
-                   : run_rows<2, 1>(a, items, grid, lse, nullptr, 0, stream);
+  if (lse) return run_rows<1, 1>(a, items, grid, lse, nullptr, 0, stream);
   return nr == 1 ? run_rows<1, 0>(a, items, grid, nullptr, nullptr, 0, stream)
                  : run_rows<2, 0>(a, items, grid, nullptr, nullptr, 0, stream);
 }

@@ -3,8 +3,9 @@
 //
 // Rotation.  theta_i = base^(-2i/128).  The workspace holds f_i = theta_i / 2 pi as a 64-bit
 // fraction of a turn, so the angle of position t is the wrapped product t * f_i: the range
-// reduction is exact integer arithmetic for every position (t < 2^30 loses less than 2^-34 of
-// a turn) and cos and sin come from sincospif of its top 32 bits.  Rotations compose,
+// reduction is exact integer arithmetic, and f_i, formed in doubles, is good to 2^-55 of a turn
+// (a position near 2^20 to 2^-35, one near 2^30 to 2^-25).  cos and sin come from sincospif of the
+// top 32 bits as a float, half a step of which is 2^-26 of a turn.  Rotations compose,
 // <R_p q, R_t k> = <R_{p-T} q, R_{t-T} k>, so a kernel that walks keys in spans of 64 from an
 // aligned T reads the keys' rotations from one table of 64 positions and turns the few query
 // rows by p - T once a span.

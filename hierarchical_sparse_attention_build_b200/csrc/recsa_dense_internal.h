@@ -61,6 +61,7 @@ inline int redo_slot(int bh, int tiles, int tile) { return (int)(((int64_t)bh * 
 
 int dense_sm_count();  // of the current device
 int launch_dense_init(void *ws, double base, void *stream);
+// The rows kernel: outputs, or with `lse` the rows' log2-sum-exp (at most 8 rows a KV group).
 int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
 // The chunk kernel (bf16 output), then the rows kernel for the items it marked; kNoRoom, with
 // nothing launched, where a head's rotated keys do not fit image_bytes of the workspace.

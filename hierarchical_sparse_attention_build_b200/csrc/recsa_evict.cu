@@ -39,7 +39,9 @@ struct SelectSmem {
 // larger weight -> larger key; NaN below every number
 __device__ __forceinline__ uint32_t weight_key(float w) { return w == w ? order_key(w) : 0u; }
 
-// PER > 0: a thread holds its weights' keys, at most PER of them; 0: they are read again each time.
+// PER > 0: a thread holds its weights' keys, at most PER of them (two blocks an SM leave it 64
+// registers: of 32 keys some lie in local memory, 172 bytes of spill stores); 0: they are read
+// again each time.
 template <int PER>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
