@@ -13,7 +13,7 @@ import torch
 
 import dense_reference as F
 import hierarchical_sparse_attention_build_b200 as R
-from test_gpu_dense import Case, check
+from test_gpu_dense import Case, check, params
 from test_gpu_dense_layers import layer
 from test_gpu_paged import paginate
 
@@ -121,3 +121,71 @@ def test_weights_follow_their_tokens_between_two_caches():
         s.evict(70, 4, 10, into=to, into_weights=tw)
         c.cap = cap
         s.weigh(s.append(60)[:, -2:].contiguous())
+
+
+def test_a_bounded_decode_step_in_one_graph():
+    """Append, attend, weigh and evict in place, captured once: replays give the eager steps' bits,
+    for sequences that reach the bound at different steps."""
+    B, H, G, keep, steps = 3, 2, 4, 40, 12
+    g = torch.Generator().manual_seed(12)
+    new = [[torch.randn(B, 1, h, 128, generator=g).bfloat16() for h in (H, H, H * G)] for _ in range(steps)]
+    results = []
+    for graph in (False, True):
+        c = Case(B, H, G, 64, 1, seed=11, page=16, lens=[38, 3, 40], garbage=0.0)
+        c.cache.length = 64  # the bound of every step
+        w = torch.zeros(B, H, c.cap, device="cuda")
+        kept = torch.empty(B, H, keep, dtype=torch.int32, device="cuda")
+        bufs = [x.cuda() for x in new[0]]
+        out = torch.empty(B, 1, H * G, 128, device="cuda")
+
+        def step():
+            c.cache.length = 64
+            R.dense_decode_step(c.p, c.cache, *bufs, out, c.ws, VIEW)
+            R.accumulate_weights(c.p, c.cache, bufs[2], w, c.ws, VIEW)
+            R.evict(c.p, c.cache, w, keep, kept, into_weights=w, sinks=2, recent=8)
+
+        if graph:
+            state = (c.cache.seq_len, c.cache.k_tok, c.cache.v_tok, w)
+            before = [x.clone() for x in state]
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                step()
+            torch.cuda.current_stream().wait_stream(s)
+            for x, y in zip(state, before):
+                x.copy_(y)
+            cg = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(cg):
+                step()
+        seen = []
+        for x in new:
+            for dst, src in zip(bufs, x):
+                dst.copy_(src)
+            cg.replay() if graph else step()
+            seen.append([t.clone() for t in (out, kept, w, c.cache.seq_len)])
+        R.check_device_errors(c.ws)
+        assert c.cache.seq_len.tolist() == [40, 15, 40] and c.cache.length == keep
+        results.append(seen + [[c.cache.k_tok, c.cache.v_tok]])
+    for a, b in zip(*results):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_a_large_batch_of_uneven_sequences():
+    """More sequences than have their steps dealt out to the blocks, and one fewer."""
+    for B in (257, 256):
+        H, G, L = 1, 4, 2000
+        lens = [(37 * b) % (L + 1) for b in range(B)]
+        lens[5] = L
+        p = params(H, G)
+        gen = torch.Generator(device="cuda").manual_seed(B)
+        k, v = (torch.empty(B, H, L, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+        q = torch.empty(B, 1, H * G, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+        cache, ws = R.TokenCache(p, k, v, L, seq_len=torch.tensor(lens, device="cuda")), R.DenseWorkspace(p, B, L, "cuda")
+        out, w = torch.empty(q.shape, device="cuda"), torch.zeros(B, H, L, device="cuda")
+        R.dense_attend(p, cache, q, out, ws)
+        R.accumulate_weights(p, cache, q, w, ws)
+        R.check_device_errors(ws)
+        want = F.attend(q, k, v, lens, G)
+        assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -16
+        want = F.attend(q, k, v, lens, G, want_weights=True)
+        assert float((w.double() - want).norm() / want.norm()) <= 2.0 ** -16
