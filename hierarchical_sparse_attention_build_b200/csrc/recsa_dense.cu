@@ -690,7 +690,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
 #pragma unroll
     for (int w = 0; w < kWarps / NR; ++w) {
       const float mw = sm.m[w0 + w][row];
-      if (mw == -INFINITY) continue;
+      if (mw == -INFINITY) {
+        sum += sm.l[w0 + w][row];  // 0, or NaN: every score was
+        continue;
+      }
       const float f = exp2_approx(mw - mx);
       sum += f * sm.l[w0 + w][row];
       if (PV) {
@@ -774,7 +777,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
 #pragma unroll
           for (int i = 0; i < kPer / 4; ++i) u[i] = __ldcg(reinterpret_cast<const float4 *>(p + 4 + d0) + i);
         }
-        if (ml.x == -INFINITY) continue;
+        if (ml.x == -INFINITY) {
+          sum += ml.y;
+          continue;
+        }
         sum += f * ml.y;
         if (PV) {
 #pragma unroll

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           for (int j = 0; j < 2 * a.parts; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
           for (int j = 0; j < 2 * a.parts; ++j) {
             const float2 v = __ldcg(src + j * kTile);
-            if (v.x != -INFINITY) l += v.y * exp2_approx(v.x - m);
+            l += v.x != -INFINITY ? v.y * exp2_approx(v.x - m) : v.y;  // (0, or NaN: every score was)
           }
           // a row that sees nothing gives no weight; neither does a row past the queries
           sm.lse[tid] = a.row0 + rt * kTile + tid < (d.nq << d.group_shift) && (l > 0.f || l != l) ? m + log2f(l) : INFINITY;
