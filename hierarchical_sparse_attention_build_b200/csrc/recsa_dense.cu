@@ -111,19 +111,28 @@ __device__ __forceinline__ void load_step(const DenseArgs &a, const uint16_t *ca
 }
 
 // The rotation table into shared memory (queued; the caller commits and waits).
-__device__ __forceinline__ void load_table(const DenseArgs &a, unsigned char *table, int tid) {
+__device__ __forceinline__ void load_table(const DenseArgs &a, unsigned char *table, bool scaled, int tid) {
   const uint32_t dst = smem_u32(table);
 #pragma unroll
   for (int i = 0; i < kSpan * kHalf / 2 / kThreads; ++i) {
     const int e = tid + i * kThreads;
     const int r = e / (kHalf / 2), piece = e % (kHalf / 2);
-    cp_async16(dst + r * kTableStride + ((piece ^ ((r & 1) << 2)) << 4), ws_table(a.hdr) + 2 * e, true);
+    cp_async16(dst + r * kTableStride + ((piece ^ ((r & 1) << 2)) << 4), ws_table(a.hdr, scaled) + 2 * e, true);
   }
 }
 
+// Two values as the first part of an operand, and what that leaves as the second: fp16 or bf16 pairs.
+template <bool HALF>
+__device__ __forceinline__ void split_pair(F2 x, uint32_t &hi, uint32_t &lo) {
+  const float2 u = f2_get(x);
+  hi = HALF ? cvt_f16x2(u.x, u.y) : cvt_bf16x2(u.x, u.y);
+  const float2 d = f2_get(f2_fma(HALF ? f2_f16(hi) : f2_bf16(hi), f2(-1.f, -1.f), x));
+  lo = HALF ? cvt_f16x2(d.x, d.y) : cvt_bf16x2(d.x, d.y);
+}
+
 // 8 query rows turned by a further `delta` positions, as the B operands of the score product: each
-// value as two bf16 parts (q rounded, and what that leaves, rounded).
-template <int NR>
+// value as two parts (q rounded, and what that leaves, rounded).
+template <int NR, bool EX>
 __device__ __forceinline__ void turn_queries(const DenseArgs &a, const float (*q)[kQStride], int delta, float4 *ang,
                                              uint32_t (&qh)[NR][16], uint32_t (&ql)[NR][16], int lane) {
   const uint64_t *f = ws_freq(a.hdr);
@@ -141,20 +150,20 @@ __device__ __forceinline__ void turn_queries(const DenseArgs &a, const float (*q
       const float2 x = *reinterpret_cast<const float2 *>(&q[nt * 8 + r][ch * 8 + 2 * c]);
       const float2 y = *reinterpret_cast<const float2 *>(&q[nt * 8 + r][ch * 8 + 2 * c + kHalf]);
       const F2 X = f2(x.x, x.y), Y = f2(y.x, y.y);
-      const float2 u = f2_get(f2_fma(Y, f2_neg(sn), f2_mul(X, cs))), v = f2_get(f2_fma(X, sn, f2_mul(Y, cs)));
-      qh[nt][ch] = cvt_bf16x2(u.x, u.y);
-      qh[nt][ch + 8] = cvt_bf16x2(v.x, v.y);
-      ql[nt][ch] = residue_bf16x2(u.x, u.y, qh[nt][ch]);
-      ql[nt][ch + 8] = residue_bf16x2(v.x, v.y, qh[nt][ch + 8]);
+      split_pair<EX>(f2_fma(Y, f2_neg(sn), f2_mul(X, cs)), qh[nt][ch], ql[nt][ch]);
+      split_pair<EX>(f2_fma(X, sn, f2_mul(Y, cs)), qh[nt][ch + 8], ql[nt][ch + 8]);
     }
   }
 }
 
 // Scores of a step's 16 keys (rows of the product) with the tile's query rows (columns): the keys
-// are rotated by their place in the span.  Both operands are two bf16 parts, hi * hi + lo * hi +
-// hi * lo: what is dropped is below 2^-16 of the product of the magnitudes.
+// are rotated by their place in the span.  Both operands are two parts, hi * hi + lo * hi +
+// hi * lo: what is dropped is below 2^-16 of the product of the magnitudes with bf16 parts, below
+// 2^-22 with fp16 ones (EX: fp32 outputs and weights).  A rotated element beyond fp16's range makes
+// the score NaN (its second part is the opposite infinity): such a row goes to careful_row.
+// The tensor cores cut sums off: with EX every 64 dimensions' high parts are joined by rounded adds.
 // s[nt]: keys lane/4 (first two) and lane/4 + 8, query rows nt * 8 + 2 (lane % 4) and one more.
-template <int NR>
+template <int NR, bool EX>
 __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t sk, int T, const uint32_t (&qh)[NR][16],
                                            const uint32_t (&ql)[NR][16], float (&s)[NR][4], int lane) {
   const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: lanes 0-15 the first 8 dimensions' rows, 16-31 the next 8
@@ -173,12 +182,28 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
       const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (((2 * ks + (i >> 1)) * 64) ^ odd));
       const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]), minus = f2(-1.f, -1.f);
       const F2 U = f2_fma(f2_mul(Y, sn), minus, f2_mul(X, cs)), V = f2_fma(X, sn, f2_mul(Y, cs));
-      const float2 u = f2_get(U), v = f2_get(V);
-      uh[i] = cvt_bf16x2(u.x, u.y);
-      vh[i] = cvt_bf16x2(v.x, v.y);
-      const float2 du = f2_get(f2_fma(f2_bf16(uh[i]), minus, U)), dv = f2_get(f2_fma(f2_bf16(vh[i]), minus, V));
-      ul[i] = cvt_bf16x2(du.x, du.y);
-      vl[i] = cvt_bf16x2(dv.x, dv.y);
+      split_pair<EX>(U, uh[i], ul[i]);
+      split_pair<EX>(V, vh[i], vl[i]);
+    }
+    if (EX) {
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
+        float t[4];
+        mma16816_half_zero(ks == 0 ? s[nt] : t, uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816_half(ks == 0 ? s[nt] : t, vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+        if (ks == 0)
+          mma16816_half_zero(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+        else
+          mma16816_half(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+        mma16816_half(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
+        mma16816_half(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816_half(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+        if (ks > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] += t[i];
+        }
+      }
+      continue;
     }
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
@@ -198,7 +223,7 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] += lo[nt][i];
+    for (int i = 0; i < 4; ++i) s[nt][i] = EX ? (s[nt][i] + lo[nt][i]) * (1.f / (kKeyScale * kQueryScale)) : s[nt][i] + lo[nt][i];
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -249,12 +274,13 @@ struct Dealt {
 };
 
 // One row over the steps [begin, stop) of its tile by one warp, in fp32: dimensions 4 lane .. 4 lane
-// + 3 of the weighted sum of values, the weights' sum and the maximum they are relative to.  Every
+// + 3 of the weighted sum of values (without PV: the scores, written), the weights' sum and the
+// maximum they are relative to.  Every
 // value is weighed by itself: one that the row does not see is not touched, and an infinity does
 // not meet the zero that a weight's second part may be.
-template <int R>
+template <int R, bool PV, bool EX>
 __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg, int row, int b, int h, int p_max,
-                            int base_sink, float (&acc)[4], float &m, float &sum) {
+                            int base_sink, int bh, float (&acc)[4], float &m, float &sum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = sm.pos[row];
   float *const turned = reinterpret_cast<float *>(sm.ang[warp]);
   const uint64_t *f = ws_freq(a.hdr);
@@ -270,7 +296,8 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
 #pragma unroll
     for (int i = lane; i < kHalf; i += 32) {  // the row turned to the span, as the keys' table is
       const float2 w = rotation(delta, __ldg(f + i));
-      const float x = sm.q[sink][row][i], y = sm.q[sink][row][i + kHalf];
+      const float x = sm.q[sink][row][i] * (EX ? 1.f / kQueryScale : 1.f),
+                  y = sm.q[sink][row][i + kHalf] * (EX ? 1.f / kQueryScale : 1.f);
       turned[i] = x * w.x - y * w.y;
       turned[i + kHalf] = y * w.x + x * w.y;
     }
@@ -285,7 +312,8 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
       const unsigned char *tr = sm.table + (t & (kSpan - 1)) * kTableStride;
 #pragma unroll 4
       for (int i = (lane >> 4) * 16; i < (lane >> 4) * 16 + 16; ++i) {
-        const float4 w = *reinterpret_cast<const float4 *>(tr + ((i ^ ((t & 1) << 2)) << 4));
+        float4 w = *reinterpret_cast<const float4 *>(tr + ((i ^ ((t & 1) << 2)) << 4));
+        if (EX) w.x *= 1.f / kKeyScale, w.y *= 1.f / kKeyScale, w.z *= 1.f / kKeyScale, w.w *= 1.f / kKeyScale;
         const uint32_t x = __ldg(key + i), y = __ldg(key + i + 32);
         s += turned[2 * i] * (bf16_lo(x) * w.x - bf16_lo(y) * w.z) + turned[2 * i + 1] * (bf16_hi(x) * w.y - bf16_hi(y) * w.w);
         s += turned[2 * i + kHalf] * (bf16_lo(y) * w.x + bf16_lo(x) * w.z) +
@@ -294,6 +322,8 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
     }
     s += __shfl_xor_sync(0xffffffffu, s, 16);
     if (r < 0) s = -INFINITY;
+    if (!PV && a.scores && row < a.score_stride && lane < kStep)
+      a.scores[((int64_t)(bh - a.bh0) * a.score_pitch + t) * a.score_stride + row] = s;
     float x = s;
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -311,8 +341,9 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
       const float w = __shfl_sync(0xffffffffu, weight, key);
       const int64_t v_row = __shfl_sync(0xffffffffu, r, key);
       if (!((seen >> key) & 1u)) continue;
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(a.v + v_row * kD) + lane);
       sum += w;
+      if (!PV) continue;
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(a.v + v_row * kD) + lane);
       acc[0] += w * bf16_lo(v.x), acc[1] += w * bf16_hi(v.x), acc[2] += w * bf16_lo(v.y), acc[3] += w * bf16_hi(v.y);
     }
   }
@@ -323,14 +354,16 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
 // they see.  Each warp walks its own steps of 16 keys with an online softmax, its keys and values
 // fetched one step ahead with cp.async into memory of its own, so warps never wait for one another
 // until their (max, sum, output) are joined at the end; the last block of a tile joins the blocks.
+// EX: fp32's accuracy (fp32 outputs, weights).  Against two bf16 parts of everything the error of 16
+// queries over 4096 tokens fell from 6e-6 to 2.8e-7 (plain fp32 arithmetic: 7.8e-7), at the same time.
 // Scores, probabilities and outputs are products of the tensor cores with keys (scores) and
 // dimensions (outputs) as rows and the query rows as columns, so that one to eight rows - a decode
 // step - fill an instruction.  DRAM and issue bound it together: a key of 512 bytes costs about 56
 // issue slots of the ~88 its SM has meanwhile (2 x 131072 tokens, 8 KV heads, G = 4: 178 us, 74 % of
 // the DRAM peak and 63 % of the slots).
-// MODE 0: the output.  MODE 1: the rows' log2-sum-exp to `lse`.  MODE 2: the output of the tiles
+// MODE 0: the output.  MODE 1: the rows' (maximum, 1 / sum) to `lse`.  MODE 2: the output of the tiles
 // that the chunk kernel marked in `redo`, if any.
-template <int NR, int MODE, bool DEAL>
+template <int NR, int MODE, bool DEAL, bool EX>
 __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     dense_rows_kernel(DenseArgs a, int items, float *lse, uint32_t *redo, int chunk_tiles) {
   constexpr int R = 8 * NR;
@@ -339,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   RowsSmem<R> &sm = *reinterpret_cast<RowsSmem<R> *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gs = a.group_shift, G = 1 << gs, hq = a.hkv << gs;
+  const float qscale = EX ? a.qscale * kQueryScale : a.qscale;
   const WsHeader head = *a.hdr;  // checked once the first loads are on their way
   if (MODE == 2) {  // nearly always nothing is marked
     uint32_t any = 0;
@@ -418,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     begin = (int)((int64_t)rg.total * split / a.nsplit);
     stop = (int)((int64_t)rg.total * (split + 1) / a.nsplit);
   }
-  if (PV && tid == 0) sm.range[0] = begin, sm.range[1] = stop;
+  if (tid == 0) sm.range[0] = begin, sm.range[1] = stop;
   // this warp's steps; the first loads are on their way while the query rows are turned
   const int st0 = begin + (int)((int64_t)(stop - begin) * warp / kWarps),
             st1 = begin + (int)((int64_t)(stop - begin) * (warp + 1) / kWarps);
@@ -428,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   };
   // MODE 1 has no values: its keys alternate between the two halves of the stage
   Step cur = {0, 0u}, next = {0, 0u};
-  if (!table) load_table(a, sm.table, tid);  // with the first step's keys
+  if (!table) load_table(a, sm.table, EX, tid);  // with the first step's keys
   table = true;
   if (st0 < st1) {
     cur = place(st0);
@@ -449,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     float x = 0.f, y = 0.f;
     if ((row >> gs) < nq) {
       const uint16_t *src = a.q + (((int64_t)b * a.nq + q0 + (row >> gs)) * hq + h * G + (row & (G - 1))) * kD + i;
-      x = __uint_as_float((uint32_t)src[0] << 16) * a.qscale;
-      y = __uint_as_float((uint32_t)src[kHalf] << 16) * a.qscale;
+      x = __uint_as_float((uint32_t)src[0] << 16) * qscale;
+      y = __uint_as_float((uint32_t)src[kHalf] << 16) * qscale;
       const int p = dense_position(a, len, q0 + (row >> gs));
       const int d = sink ? sink_position(a, p) - base_sink : p - p_max;
       if (d != 0) {
@@ -494,13 +528,13 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
     const int span = (T / kSpan) * 2 + (sink ? 1 : 0);
     if (span != turned) {
       turned = span;
-      turn_queries<NR>(a, sm.q[sink], (sink ? base_sink : p_max) - a.back - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
+      turn_queries<NR, EX>(a, sm.q[sink], (sink ? base_sink : p_max) - a.back - (T & ~(kSpan - 1)), sm.ang[warp], qh, ql, lane);
     }
     cp_async_wait<1>();
     __syncwarp();
     float s[NR][4];
     const uint32_t keys = PV || !(st & 1) ? sk : sv;
-    score_step<NR>(sm.table, keys, T, qh, ql, s, lane);
+    score_step<NR, EX>(sm.table, keys, T, qh, ql, s, lane);
     __syncwarp();  // the keys' memory is free
     const uint32_t live = cur.live;
     constexpr int kAhead = PV ? 1 : 2;
@@ -615,14 +649,17 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
           __syncwarp();
         }
       }
-      uint32_t ph[NR][2], pl[NR][2];  // the weights with keys along the k of the product
+      uint32_t ph[NR][2], pl[NR][2], pm[NR][2];  // the weights' parts with keys along the k of the product
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t hi = cvt_bf16x2(s[nt][2 * k], s[nt][2 * k + 1]);
           ph[nt][k] = transpose8x8(hi);
-          pl[nt][k] = transpose8x8(residue_bf16x2(s[nt][2 * k], s[nt][2 * k + 1], hi));
+          const uint32_t lo = residue_bf16x2(s[nt][2 * k], s[nt][2 * k + 1], hi);
+          pl[nt][k] = transpose8x8(lo);
+          if (EX)
+            pm[nt][k] = transpose8x8(residue_bf16x2(s[nt][2 * k] - bf16_lo(hi), s[nt][2 * k + 1] - bf16_hi(hi), lo));
         }
       const int key = (lane & 7) + ((lane >> 4) << 3), dch = (lane >> 3) & 1;
 #pragma unroll
@@ -635,7 +672,12 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
           // keys an output summed there alone came out 5e-5 short.  A step's 16 keys are
           // summed there, the steps in fp32 adds that round.
           float t[4];
-          mma16816_zero(t, v, pl[nt][0], pl[nt][1]);
+          if (EX) {
+            mma16816_zero(t, v, pm[nt][0], pm[nt][1]);
+            mma16816(t, v, pl[nt][0], pl[nt][1]);
+          } else {
+            mma16816_zero(t, v, pl[nt][0], pl[nt][1]);
+          }
           mma16816(t, v, ph[nt][0], ph[nt][1]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[PV ? nt : 0][d][i] += t[i];
@@ -705,17 +747,17 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
       }
     }
   }
-  if (PV) {  // (a row's threads are lanes of one warp)
-    float size = 0.f;
+  {  // (a row's threads are lanes of one warp)
+    float size = sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) size += fabsf(acc[i]);
+    for (int i = 0; i < kPer; ++i) size += PV ? fabsf(acc[i]) : 0.f;
     const uint32_t large = __ballot_sync(0xffffffffu, !(size <= kRowsLarge));
     if (large) {
 #pragma unroll 1
       for (int j = 0; j < NR; ++j) {
         if (!(large >> (j * (32 / NR)) << (32 - 32 / NR))) continue;
         float x[4], xm, xsum;
-        careful_row<R>(a, sm, rg, warp * NR + j, b, h, p_max, base_sink, x, xm, xsum);
+        careful_row<R, PV, EX>(a, sm, rg, warp * NR + j, b, h, p_max, base_sink, bh, x, xm, xsum);
         const bool mine = row == warp * NR + j;
         if (mine) mx = xm, sum = xsum;
 #pragma unroll
@@ -795,8 +837,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1)
   if (write && (row >> gs) < nq) {
     const int64_t out_row = ((int64_t)b * a.nq + q0 + (row >> gs)) * hq + h * G + (row & (G - 1));
     if (!PV) {
-      // no key: every weight is exp2(-inf)
-      if (d0 == 0) lse[out_row] = sum > 0.f || sum != sum ? mx + log2f(sum) : INFINITY;
+      // a key's weight is exp2(score - maximum) / sum: no logarithm of the sum, whose rounding would
+      // weigh on every weight of the row
+      if (d0 == 0)
+        reinterpret_cast<float2 *>(lse)[out_row] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(mx, 1.f / sum);
     } else {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -861,6 +905,8 @@ __global__ void dense_init_kernel(unsigned char *ws, double base) {
     float *w = reinterpret_cast<float *>(ws + kDenseTable) + (r * kHalf + (i & ~1)) * 2 + (i & 1);
     w[0] = (float)c;  // two frequencies: cos, cos', sin, sin'
     w[2] = (float)s;
+    w[kDenseTableBytes / sizeof(float)] = (float)(c * kKeyScale);
+    w[kDenseTableBytes / sizeof(float) + 2] = (float)(s * kKeyScale);
   }
   if (r == 0) {
     const double turns = theta / (2.0 * 3.14159265358979323846);
@@ -888,11 +934,11 @@ int opt_in(K kernel, size_t bytes) {
 // Blocks of the rows kernel an SM holds.
 constexpr int blocks_per_sm(int nr) { return nr == 1 ? 2 : 1; }
 
-template <int NR, int MODE, bool DEAL = false>
+template <int NR, int MODE, bool DEAL, bool EX>
 int run_rows(const DenseArgs &a, int64_t items, int64_t grid, float *lse, uint32_t *redo, int chunk_tiles, void *stream) {
-  const int rc = opt_in(dense_rows_kernel<NR, MODE, DEAL>, sizeof(RowsSmem<8 * NR>));
+  const int rc = opt_in(dense_rows_kernel<NR, MODE, DEAL, EX>, sizeof(RowsSmem<8 * NR>));
   if (rc) return rc;
-  dense_rows_kernel<NR, MODE, DEAL><<<(unsigned)grid, kThreads, sizeof(RowsSmem<8 * NR>), (cudaStream_t)stream>>>(
+  dense_rows_kernel<NR, MODE, DEAL, EX><<<(unsigned)grid, kThreads, sizeof(RowsSmem<8 * NR>), (cudaStream_t)stream>>>(
       a, (int)items, lse, redo, chunk_tiles);
   return (int)cudaGetLastError();
 }
@@ -936,6 +982,16 @@ static int pick_split(int64_t items, int64_t max_keys, int places, int rows) {
   return best;
 }
 
+template <bool DEAL>
+static int run_rows_as(const DenseArgs &a, int nr, int64_t items, int64_t grid, float *lse, void *stream) {
+  if (lse) return run_rows<1, 1, DEAL, true>(a, items, grid, lse, nullptr, 0, stream);
+  if (a.out_fp32)
+    return nr == 1 ? run_rows<1, 0, DEAL, true>(a, items, grid, nullptr, nullptr, 0, stream)
+                   : run_rows<2, 0, DEAL, true>(a, items, grid, nullptr, nullptr, 0, stream);
+  return nr == 1 ? run_rows<1, 0, DEAL, false>(a, items, grid, nullptr, nullptr, 0, stream)
+                 : run_rows<2, 0, DEAL, false>(a, items, grid, nullptr, nullptr, 0, stream);
+}
+
 int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
   // Tiles of 8 rows keep two blocks on an SM; more rows than that share a key's fetch and turn.
   const int nr = ((int64_t)a.nq << a.group_shift) <= 8 ? 1 : 2;
@@ -949,15 +1005,10 @@ int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream) {
   const int64_t steps = all * (ceil_div(max_keys, kStep) + 2);
   if (a.seq_len && steps >= 64 * (int64_t)places && steps < (int64_t)1 << 31 && a.tiles == 1 && a.batch <= kDealtSequences && items == all && items <= kMaxShared) {
     a.nsplit = 1;
-    if (lse) return run_rows<1, 1, true>(a, items, places, lse, nullptr, 0, stream);
-    return nr == 1 ? run_rows<1, 0, true>(a, items, places, nullptr, nullptr, 0, stream)
-                   : run_rows<2, 0, true>(a, items, places, nullptr, nullptr, 0, stream);
+    return run_rows_as<true>(a, nr, items, places, lse, stream);
   }
   a.nsplit = pick_split(items, max_keys, places, 8 * nr);
-  const int64_t grid = items * a.nsplit;
-  if (lse) return run_rows<1, 1>(a, items, grid, lse, nullptr, 0, stream);
-  return nr == 1 ? run_rows<1, 0>(a, items, grid, nullptr, nullptr, 0, stream)
-                 : run_rows<2, 0>(a, items, grid, nullptr, nullptr, 0, stream);
+  return run_rows_as<false>(a, nr, items, items * a.nsplit, lse, stream);
 }
 
 int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream) {
@@ -966,7 +1017,7 @@ int launch_dense_redo(DenseArgs a, int chunk_tiles, void *stream) {
   a.nsplit = 1;
   const int64_t items = (int64_t)a.batch * a.hkv * a.tiles;
   uint32_t *redo = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(a.hdr) + kDenseRedo);
-  return run_rows<2, 2>(a, items, std::min<int64_t>(items, dense_sm_count()), nullptr, redo, chunk_tiles, stream);
+  return run_rows<2, 2, false, false>(a, items, std::min<int64_t>(items, dense_sm_count()), nullptr, redo, chunk_tiles, stream);
 }
 
 int launch_append_tokens(const DenseArgs &a, void *k, void *v, const void *k_new, const void *v_new, int64_t at,

@@ -19,8 +19,9 @@ namespace recsa {
 __device__ __forceinline__ const uint64_t *ws_freq(const WsHeader *h) {
   return reinterpret_cast<const uint64_t *>(reinterpret_cast<const char *>(h) + kDenseFreq);
 }
-__device__ __forceinline__ const float2 *ws_table(const WsHeader *h) {
-  return reinterpret_cast<const float2 *>(reinterpret_cast<const char *>(h) + kDenseTable);
+__device__ __forceinline__ const float2 *ws_table(const WsHeader *h, bool scaled) {
+  return reinterpret_cast<const float2 *>(reinterpret_cast<const char *>(h) + kDenseTable +
+                                          (scaled ? kDenseTableBytes : 0));
 }
 __device__ __forceinline__ int32_t *ws_count(WsHeader *h) {
   return reinterpret_cast<int32_t *>(reinterpret_cast<char *>(h) + kDenseCount);
@@ -89,7 +90,23 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t &a, uint32_t
                : "r"(addr)
                : "memory");
 }
-// c += a (16 x 16, row) * b (16 x 8, column), bf16 operands, fp32 sums
+// c += a (16 x 16, row) * b (16 x 8, column), fp16 operands, fp32 sums
+__device__ __forceinline__ void mma16816_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c = a * b, fp16 operands
+__device__ __forceinline__ void mma16816_half_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// the same with bf16 operands
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -114,6 +131,12 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 // what the rounding of (lo, hi) to the packed pair `r` left over, itself rounded to bf16
 __device__ __forceinline__ uint32_t residue_bf16x2(float lo, float hi, uint32_t r) {
   return cvt_bf16x2(lo - bf16_lo(r), hi - bf16_hi(r));
+}
+// the same for fp16
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 // Two fp32 lanes in one register pair: one instruction an operation on both.
 struct F2 {
@@ -146,6 +169,13 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 f2_neg(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
 __device__ __forceinline__ F2 f2_bf16(uint32_t u) { return f2(bf16_lo(u), bf16_hi(u)); }
+__device__ __forceinline__ F2 f2_f16(uint32_t u) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(u));
+  return f2(lo, hi);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

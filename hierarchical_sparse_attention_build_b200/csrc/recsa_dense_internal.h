@@ -10,12 +10,13 @@
 
 namespace recsa {
 
-constexpr uint32_t kDenseMagic = 0x52534432u;  // "RSD2"
+constexpr uint32_t kDenseMagic = 0x52534433u;  // "RSD3"
 constexpr int kSpan = 64;                      // positions of the rotation table
 constexpr int kMaxShared = 4096;               // work items whose key range may be shared by blocks
 constexpr size_t kDenseFreq = kWsHeader;                                   // uint64[64] turns
 constexpr size_t kDenseTable = kDenseFreq + kHalf * sizeof(uint64_t);      // float4[64][32] (cos, cos', sin, sin')
-constexpr size_t kDenseCount = kDenseTable + kSpan * kHalf * 2 * sizeof(float);
+constexpr size_t kDenseTableBytes = kSpan * kHalf * 2 * sizeof(float);
+constexpr size_t kDenseCount = kDenseTable + 2 * kDenseTableBytes;  // (the second table: the first times kKeyScale)
 constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t) + 256;  // marks of items to compute again
 constexpr size_t kDensePrefix = kDenseRedo + kMaxShared * sizeof(uint32_t);  // key tiles before each item of a chunk
 constexpr size_t kDensePart = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // partial results
@@ -28,6 +29,9 @@ constexpr size_t kMaxHeadImages = (size_t)1280 << 20;   // for one long head
 constexpr int kPartRow = kD + 4;  // floats of a row's partial result: maximum, sum, 2 unused, 128 sums
 
 constexpr float kLog2e = 1.4426950408889634f;
+// fp32 outputs and weights are scored from two fp16 parts of rotated rows, 22 bits, of keys and
+// queries times these powers of two: the parts' smallest steps are then 2^-29 and 2^-31.
+constexpr float kKeyScale = 16.f, kQueryScale = 64.f;
 
 // The cache and the queries of one launch.
 struct DenseArgs {

@@ -1,7 +1,8 @@
 // The softmax weight each cache slot receives: w[t] = sum over query rows of exp2(s[row][t] - L[row]),
 // L[row] the row's log2-sum-exp.  Every weight needs every row's sum, so the scores are needed twice.
 //
-// A few rows (a decode step: at most 8 a KV group): reading K bounds it.  The rows kernel leaves
+// A few rows (a decode step: at most 8 a KV group): reading K bounds it.  The rows kernel (in its
+// accurate form) leaves
 // its scores (4 bytes a row and key, against the key's 256) with the sums, and a second pass turns
 // them into weights: weights of one step over 4 x 65536 tokens took 394 us with K read twice.
 //
@@ -391,18 +392,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
 }
 
 // Weights from the scores that the rows kernel left: a thread a key.
-__global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, const float *__restrict__ lse,
+__global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, const float2 *__restrict__ sums,
                                                                  float *__restrict__ weights, int accumulate) {
   if (a.hdr->magic != kDenseMagic || a.hdr->rope_base != a.rope_base) return;  // the rows kernel reported it
   const int bh = a.bh0 + blockIdx.y, b = bh / a.hkv, h = bh % a.hkv, gs = a.group_shift, G = 1 << gs;
   const int len = dense_length(a, b, false), rows = a.nq << gs;
-  __shared__ float z[8];
+  __shared__ float2 z[8];  // a row's maximum and 1 / sum
   __shared__ int pos[8];  // the rows kernel visits no token that no row sees
   if (threadIdx.x < 8) {
     pos[threadIdx.x] = threadIdx.x < rows ? dense_position(a, len, threadIdx.x >> gs) : 0;
-    z[threadIdx.x] = threadIdx.x < rows ? lse[((int64_t)b * a.nq + (threadIdx.x >> gs)) * (a.hkv << gs) + h * G +
-                                              (threadIdx.x & (G - 1))]
-                                        : INFINITY;
+    z[threadIdx.x] = threadIdx.x < rows ? sums[((int64_t)b * a.nq + (threadIdx.x >> gs)) * (a.hkv << gs) + h * G +
+                                               (threadIdx.x & (G - 1))]
+                                        : make_float2(0.f, 0.f);
   }
   __syncthreads();
   const float *s = a.scores + (int64_t)blockIdx.y * a.score_pitch * a.score_stride;
@@ -411,8 +412,8 @@ __global__ void __launch_bounds__(256) weights_from_scores_kernel(DenseArgs a, c
     float v = 0.f;
     for (int i = 0; i < a.score_stride; i += 2) {
       const float2 x = __ldcs(reinterpret_cast<const float2 *>(s + (int64_t)t * a.score_stride + i));
-      if (t < pos[i]) v += exp2_approx(x.x - z[i]);
-      if (t < pos[i + 1]) v += exp2_approx(x.y - z[i + 1]);
+      if (t < pos[i]) v += exp2_approx(x.x - z[i].x) * z[i].y;
+      if (t < pos[i + 1]) v += exp2_approx(x.y - z[i + 1].x) * z[i + 1].y;
     }
     w[t] = accumulate ? w[t] + v : v;
   }
@@ -433,7 +434,7 @@ int few_rows(DenseArgs d, float *lse, float *weights, int accumulate, int64_t ro
     const int rc = launch_dense_rows(d, d.length, lse, stream);
     if (rc) return rc;
     const dim3 grid((unsigned)std::min<int64_t>(ceil_div(d.score_pitch, 256), 4096), (unsigned)d.heads);
-    weights_from_scores_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(d, lse, weights, accumulate);
+    weights_from_scores_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(d, reinterpret_cast<const float2 *>(lse), weights, accumulate);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return (int)e;
   }
@@ -444,7 +445,7 @@ int few_rows(DenseArgs d, float *lse, float *weights, int accumulate, int64_t ro
 
 int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int accumulate, int64_t room, void *stream) {
   const int64_t rows = (int64_t)d.nq << d.group_shift, heads = (int64_t)d.batch * d.hkv;
-  if (rows <= 8 && rows * heads <= kMaxDenseLse) {
+  if (rows <= 8 && 2 * rows * heads <= kMaxDenseLse) {
     const int rc = few_rows(d, lse, weights, accumulate, room, stream);
     if (rc != kNoRoom) return rc;
   }

@@ -83,14 +83,17 @@ RECSA_API recsa_status recsa_dense_workspace_init(const recsa_params *params, in
 /* Attention of num_queries queries per sequence over the tokens that are in the cache.
  *   q   : bf16 [batch][num_queries][Hq][128], pre-RoPE.
  *   out : [batch][num_queries][Hq][128], fp32 if out_is_fp32 else bf16.
- * Accuracy.  The rows kernel, and so every fp32 output, keeps two bf16 parts of rotated rows and
- * probabilities on the tensor cores: a score is off by at most 3 * 2^-16 softmax_scale |q| |k|,
- * an output by twice that and 2^-16 of the largest value seen.  The chunk kernel rounds rotated
- * rows to fp16 and probabilities to bf16: 2^-10 softmax_scale |q| |k|, and 2^-8 beside the
- * output's own rounding.  Errors so grow with the scores; measured on random rows, as shares of
- * the output's norm (and of the worst row's):
+ * Accuracy.  fp32 outputs come from two fp16 parts of rotated rows (22 bits) and three bf16 parts
+ * of probabilities on the tensor cores, as accurate as fp32 arithmetic; rows with elements that
+ * those parts do not hold (keys beyond 4094, queries beyond about 8000 at the default scale) are
+ * computed in fp32, two to three times slower.  bf16 outputs of the rows kernel come from two bf16
+ * parts: a score is off by at most 3 * 2^-16 softmax_scale |q| |k|, an output by twice that, 2^-16
+ * of the largest value seen and its own rounding.  The chunk kernel rounds rotated rows to fp16 and
+ * probabilities to bf16: 2^-10 softmax_scale |q| |k|, and 2^-8 beside the output's own rounding.
+ * Errors so grow with the scores; measured on random rows, as shares of the output's norm (and of
+ * the worst row's):
  *   spread of the scores        1                    5                    20
- *   fp32 output           4e-6 (9e-6)          1.1e-5 (5e-5)        2.8e-5 (1.8e-4)
+ *   fp32 output           1.8e-7 (4e-7)        4.5e-7 (2.4e-6)      1.6e-6 (7e-6)
  *   bf16, rows kernel     1.7e-3 (2.2e-3)      1.7e-3 (2.3e-3)      1.4e-3 (2.2e-3)
  *   bf16, chunk kernel    2.4e-3 (3.6e-3)      2.4e-3 (5.0e-3)      2.4e-3 (1.2e-2)
  * The automatic choice goes by the sizes of the whole call; view->kernel = 1 keeps a query's
@@ -121,7 +124,8 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
 
 /* The softmax weight that each cache slot receives from the queries, summed over the queries
  * and over the query heads of its KV group, in fp32.
- * Scores are as accurate as those of an fp32 output above.
+ * Up to 8 query rows a KV group, weights are as accurate as fp32 outputs above; with more, scores
+ * come from two bf16 parts (2^-16).
  *   weights : fp32 [batch][Hkv][capacity]; slots [0, L) are overwritten (accumulate = 0) or
  *             added to (accumulate = 1), slots at or past a sequence's L are left as they are.
  * Views with a window are RECSA_ERR_UNSUPPORTED, and so are more than 8 query rows a KV group
