@@ -121,15 +121,6 @@ __device__ __forceinline__ void load_table(const DenseArgs &a, unsigned char *ta
   }
 }
 
-// Two values as the first part of an operand, and what that leaves as the second: fp16 or bf16 pairs.
-template <bool HALF>
-__device__ __forceinline__ void split_pair(F2 x, uint32_t &hi, uint32_t &lo) {
-  const float2 u = f2_get(x);
-  hi = HALF ? cvt_f16x2(u.x, u.y) : cvt_bf16x2(u.x, u.y);
-  const float2 d = f2_get(f2_fma(HALF ? f2_f16(hi) : f2_bf16(hi), f2(-1.f, -1.f), x));
-  lo = HALF ? cvt_f16x2(d.x, d.y) : cvt_bf16x2(d.x, d.y);
-}
-
 // 8 query rows turned by a further `delta` positions, as the B operands of the score product: each
 // value as two parts (q rounded, and what that leaves, rounded).
 template <int NR, bool EX>
@@ -161,7 +152,7 @@ __device__ __forceinline__ void turn_queries(const DenseArgs &a, const float (*q
 // hi * lo: what is dropped is below 2^-16 of the product of the magnitudes with bf16 parts, below
 // 2^-22 with fp16 ones (EX: fp32 outputs and weights).  A rotated element beyond fp16's range makes
 // the score NaN (its second part is the opposite infinity): such a row goes to careful_row.
-// The tensor cores cut sums off: with EX every 64 dimensions' high parts are joined by rounded adds.
+// The tensor cores cut sums off: with EX the high parts are joined by rounded adds every 32 dimensions.
 // s[nt]: keys lane/4 (first two) and lane/4 + 8, query rows nt * 8 + 2 (lane % 4) and one more.
 template <int NR, bool EX>
 __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t sk, int T, const uint32_t (&qh)[NR][16],
@@ -185,45 +176,41 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
       split_pair<EX>(U, uh[i], ul[i]);
       split_pair<EX>(V, vh[i], vl[i]);
     }
-    if (EX) {
 #pragma unroll
-      for (int nt = 0; nt < NR; ++nt) {
-        float t[4];
-        mma16816_half_zero(ks == 0 ? s[nt] : t, uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
-        mma16816_half(ks == 0 ? s[nt] : t, vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+    for (int nt = 0; nt < NR; ++nt) {
+      float t[4];  // EX: these dimensions' high parts
+      if (EX) {
+        mma16816_half_zero(t, uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816_half(t, vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
         if (ks == 0)
-          mma16816_half_zero(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+          mma16816_half_zero(lo[nt], uh, ql[nt][0], ql[nt][1]);
         else
           mma16816_half(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
         mma16816_half(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
         mma16816_half(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
         mma16816_half(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
-        if (ks > 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] += t[i];
-        }
-      }
-      continue;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      if (ks == 0) {
-        mma16816_zero(s[nt], uh, qh[nt][0], qh[nt][1]);
-        mma16816_zero(lo[nt], uh, ql[nt][0], ql[nt][1]);
+        for (int i = 0; i < 4; ++i) s[nt][i] = ks == 0 ? t[i] : s[nt][i] + t[i];
       } else {
-        mma16816(s[nt], uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
-        mma16816(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+        if (ks == 0) {
+          mma16816_zero(s[nt], uh, qh[nt][0], qh[nt][1]);
+          mma16816_zero(lo[nt], uh, ql[nt][0], ql[nt][1]);
+        } else {
+          mma16816(s[nt], uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+          mma16816(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+        }
+        mma16816(s[nt], vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+        mma16816(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
+        mma16816(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
       }
-      mma16816(s[nt], vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
-      mma16816(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
-      mma16816(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
-      mma16816(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
     }
   }
+  constexpr float kUnscale = EX ? 1.f / (kKeyScale * kQueryScale) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = EX ? (s[nt][i] + lo[nt][i]) * (1.f / (kKeyScale * kQueryScale)) : s[nt][i] + lo[nt][i];
+    for (int i = 0; i < 4; ++i) s[nt][i] = (s[nt][i] + lo[nt][i]) * kUnscale;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {

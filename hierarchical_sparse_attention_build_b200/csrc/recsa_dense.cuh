@@ -176,6 +176,14 @@ __device__ __forceinline__ F2 f2_f16(uint32_t u) {
       : "r"(u));
   return f2(lo, hi);
 }
+// Two values as the first part of an operand, and what that leaves as the second: fp16 or bf16 pairs.
+template <bool HALF>
+__device__ __forceinline__ void split_pair(F2 x, uint32_t &hi, uint32_t &lo) {
+  const float2 u = f2_get(x);
+  hi = HALF ? cvt_f16x2(u.x, u.y) : cvt_bf16x2(u.x, u.y);
+  const float2 d = f2_get(f2_fma(HALF ? f2_f16(hi) : f2_bf16(hi), f2(-1.f, -1.f), x));
+  lo = HALF ? cvt_f16x2(d.x, d.y) : cvt_bf16x2(d.x, d.y);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

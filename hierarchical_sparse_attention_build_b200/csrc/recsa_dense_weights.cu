@@ -2,17 +2,20 @@
 // L[row] the row's log2-sum-exp.  Every weight needs every row's sum, so the scores are needed twice.
 //
 // A few rows (a decode step: at most 8 a KV group): reading K bounds it.  The rows kernel (in its
-// accurate form) leaves
-// its scores (4 bytes a row and key, against the key's 256) with the sums, and a second pass turns
-// them into weights: weights of one step over 4 x 65536 tokens took 394 us with K read twice.
+// accurate form) leaves its scores (4 bytes a row and key, against the key's 256) with the sums, and
+// a second pass turns them into weights: one step's weights over 4 x 65536 tokens took 394 us with K
+// read twice.
 //
 // More rows (a prompt's last queries): the products bound it.  dense_scores_kernel forms them on
 // tcgen05 twice, with 128 x 128 tiles of keys and rows that were rotated once into shared-memory
 // images.  Pass 1 has the query rows as the product's rows, so that a thread sums a row; pass 2 has
 // the keys as rows, so that a thread sums a key over all query rows, in a fixed order and without a
-// shuffle or an atomic.  The weights are fp32, so both operands are two bf16 parts (rounded, and what
-// that leaves, rounded) and three products are summed; what is dropped is below 2^-16 of the
-// product of the magnitudes.
+// shuffle or an atomic.  The weights are fp32, so both operands are two fp16 parts (rounded, and what
+// that leaves, rounded) of scaled values and three products are summed; what is dropped is below
+// 2^-22 of the product of the magnitudes.  The tensor cores cut their sums off, toward zero, by up
+// to 2^-23 a product: a score is summed in two accumulators of 64 dimensions each, joined by a
+// rounded add (in one, 64 queries' weights over 32768 tokens were off by 1.2e-6).  A head with
+// elements that fp16 does not hold has its images made again, as two bf16 parts (2^-16).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,6 +34,9 @@ constexpr int kMaxRange = 40;               // key tiles of a block
 constexpr int64_t kCachedImages = (int64_t)80 << 20;  // of the 126 MB of L2
 constexpr int kTurnThreads = 128;
 constexpr int kTurnRows = 32;               // query rows a block of the images kernel turns
+constexpr int kParts = kTile / kTurnRows;   // blocks of a row tile
+constexpr int kWideBlocks = 32;             // blocks a head that make its images again
+constexpr float kUnscale = 1.f / (kKeyScale * kQueryScale);
 
 struct ScoreArgs {
   DenseArgs d;
@@ -41,6 +47,8 @@ struct ScoreArgs {
   int part0, parts;            // this launch's first of all blocks that a head's keys have in turn
   unsigned char *key_images, *query_images;  // [heads][key_tiles], [heads][row_tiles]: two parts each
   uint4 *live;                 // a key tile's tokens that were loaded
+  int *beyond;                 // [heads][key_tiles + kParts row_tiles]: an image's rows exceed fp16
+  int *wide;                   // [heads]: the head's images are bf16 parts
   float2 *sums;                // [heads][row_tiles][2 parts][128]: a row's (maximum, sum) in part of the keys
   float *weights;
   int accumulate;
@@ -50,7 +58,7 @@ struct ScoreSmem {
   unsigned char q[kPartBytes];
   unsigned char k[2][kPartBytes];
   float acc[kMaxRange * kTile];  // pass 2: the block's keys
-  alignas(16) float lse[kTile];
+  alignas(16) float top[kTile], inv[kTile];  // pass 2: the rows' maxima and 1 / sums
   alignas(16) int pos[kTile];
   alignas(16) uint64_t q_full;
   uint64_t q_empty, k_full[2], k_empty[2], d_full[2], d_empty[2], drain;
@@ -58,25 +66,25 @@ struct ScoreSmem {
 };
 constexpr size_t kScoreSmem = sizeof(ScoreSmem) + 1024;
 
-// One row of 8 + 8 dimensions, turned, as two bf16 parts of a tile.
-template <bool SCALE>
+// One row of 8 + 8 dimensions, times `scale`, turned, as two parts of a tile (fp16, or WIDE: bf16);
+// `most` keeps the largest magnitude.
+template <bool WIDE>
 __device__ __forceinline__ void put_parts(unsigned char *tile, int row, int ch, const uint4 &lo, const uint4 &hi,
-                                          const Turn &t, float scale) {
+                                          const Turn &t, float scale, float &most) {
   const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
   uint32_t uh[4], ul[4], vh[4], vl[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     F2 p = f2_bf16(x[i]), q = f2_bf16(y[i]);
-    if (SCALE) {
-      p = f2_mul(p, f2(scale, scale));
-      q = f2_mul(q, f2(scale, scale));
+    p = f2_mul(p, f2(scale, scale));
+    q = f2_mul(q, f2(scale, scale));
+    const F2 u = f2_fma(q, f2_neg(t.s[i]), f2_mul(p, t.c[i])), v = f2_fma(p, t.s[i], f2_mul(q, t.c[i]));
+    if (!WIDE) {
+      const float2 x = f2_get(u), y = f2_get(v);
+      most = max3(most, max3(fabsf(x.x), fabsf(x.y), fabsf(y.x)), fabsf(y.y));
     }
-    const float2 u = f2_get(f2_fma(q, f2_neg(t.s[i]), f2_mul(p, t.c[i])));
-    const float2 v = f2_get(f2_fma(p, t.s[i], f2_mul(q, t.c[i])));
-    uh[i] = cvt_bf16x2(u.x, u.y);
-    vh[i] = cvt_bf16x2(v.x, v.y);
-    ul[i] = residue_bf16x2(u.x, u.y, uh[i]);
-    vl[i] = residue_bf16x2(v.x, v.y, vh[i]);
+    split_pair<!WIDE>(u, uh[i], ul[i]);
+    split_pair<!WIDE>(v, vh[i], vl[i]);
   }
   put_row(tile, row, ch, make_uint4(uh[0], uh[1], uh[2], uh[3]), make_uint4(vh[0], vh[1], vh[2], vh[3]));
   put_row(tile + kTileBytes, row, ch, make_uint4(ul[0], ul[1], ul[2], ul[3]), make_uint4(vl[0], vl[1], vl[2], vl[3]));
@@ -88,39 +96,41 @@ __device__ __forceinline__ int row_position(const DenseArgs &d, int len, int row
   return qi < d.nq ? dense_position(d, len, qi) : 0;
 }
 
-// The first heads * key_tiles blocks turn a key tile each, the others kTurnRows query rows.
-__global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(ScoreArgs a) {
+// kTurnRows query rows into their image.
+template <bool WIDE>
+__device__ __forceinline__ void turn_query_rows(const ScoreArgs &a, int hl, int rt, int part, int lt, float &most) {
   const DenseArgs &d = a.d;
-  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the score kernel reports it
-  const int lt = threadIdx.x, ch = lt & 7, r0 = lt >> 3, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
+  const int ch = lt & 7, r0 = lt >> 3, gs = d.group_shift, G = 1 << gs, hq = d.hkv << gs;
   const uint64_t *f = ws_freq(d.hdr) + ch * 8;
-  const int keys = a.heads * a.key_tiles;
-  if ((int)blockIdx.x >= keys) {
-    constexpr int kParts = kTile / kTurnRows;
-    const int e = blockIdx.x - keys, image = e / kParts, hl = image / a.row_tiles, rt = image % a.row_tiles;
-    const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
-    const int len = dense_length(d, b, false);
+  const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
+  const int len = dense_length(d, b, false);
 #pragma unroll
-    for (int i = 0; i < kTurnRows / 16; ++i) {
-      const int in_tile = e % kParts * kTurnRows + r0 + 16 * i, row = a.row0 + rt * kTile + in_tile, qi = row >> gs;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (qi < d.nq) {
-        const uint4 *src =
-            reinterpret_cast<const uint4 *>(d.q + (((int64_t)b * d.nq + qi) * hq + h * G + (row & (G - 1))) * kD);
-        lo = __ldg(src + ch);
-        hi = __ldg(src + ch + 8);
-      }
-      Turn t;
-      t.set(f, dense_position(d, len, qi) - d.back);
-      put_parts<true>(a.query_images + (int64_t)image * kPartBytes, in_tile, ch, lo, hi, t, d.qscale);
+  for (int i = 0; i < kTurnRows / 16; ++i) {
+    const int in_tile = part * kTurnRows + r0 + 16 * i, row = a.row0 + rt * kTile + in_tile, qi = row >> gs;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (qi < d.nq) {
+      const uint4 *src =
+          reinterpret_cast<const uint4 *>(d.q + (((int64_t)b * d.nq + qi) * hq + h * G + (row & (G - 1))) * kD);
+      lo = __ldg(src + ch);
+      hi = __ldg(src + ch + 8);
     }
-    return;
+    Turn t;
+    t.set(f, dense_position(d, len, qi) - d.back);
+    put_parts<WIDE>(a.query_images + ((int64_t)hl * a.row_tiles + rt) * kPartBytes, in_tile, ch, lo, hi, t,
+                    WIDE ? d.qscale : d.qscale * kQueryScale, most);
   }
-  const int hl = blockIdx.x / a.key_tiles, kt = blockIdx.x % a.key_tiles;
+}
+
+// A key tile into its image; false where the sequence has no tokens of it.
+template <bool WIDE>
+__device__ __forceinline__ bool turn_keys(const ScoreArgs &a, int hl, int kt, int lt, float &most) {
+  const DenseArgs &d = a.d;
+  const int ch = lt & 7, r0 = lt >> 3;
+  const uint64_t *f = ws_freq(d.hdr) + ch * 8;
   const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
   const int len = dense_length(d, b, false), T = (a.key0 + kt) * kTile;
-  if (T >= len) return;
-  unsigned char *const tile = a.key_images + (int64_t)blockIdx.x * kPartBytes;
+  if (T >= len) return false;
+  unsigned char *const tile = a.key_images + ((int64_t)hl * a.key_tiles + kt) * kPartBytes;
   uint32_t word[4] = {0u, 0u, 0u, 0u};
   Turn t, step;
   t.set(f, T + r0);
@@ -147,10 +157,11 @@ __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(Sco
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      put_parts<false>(tile, r0 + 16 * (i0 + i), ch, xl[i], xh[i], t, 1.f);
+      put_parts<WIDE>(tile, r0 + 16 * (i0 + i), ch, xl[i], xh[i], t, WIDE ? 1.f : kKeyScale, most);
       t.advance(step);
     }
   }
+  if (WIDE) return true;  // (the loaded tokens are noted already)
   __shared__ uint32_t words[4];
   if (lt < 4) words[lt] = 0u;
   __syncthreads();
@@ -158,7 +169,48 @@ __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(Sco
   for (int w = 0; w < 4; ++w)
     if (ch == 0) atomicOr(&words[w], word[w]);
   __syncthreads();
-  if (lt == 0) a.live[blockIdx.x] = make_uint4(words[0], words[1], words[2], words[3]);
+  if (lt == 0) a.live[(int64_t)hl * a.key_tiles + kt] = make_uint4(words[0], words[1], words[2], words[3]);
+  return true;
+}
+
+// The first heads * key_tiles blocks turn a key tile each, the others kTurnRows query rows.
+__global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(ScoreArgs a) {
+  const DenseArgs &d = a.d;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the score kernel reports it
+  const int lt = threadIdx.x, keys = a.heads * a.key_tiles, per = a.key_tiles + kParts * a.row_tiles;
+  float most = 0.f;
+  int hl, image;
+  if ((int)blockIdx.x >= keys) {
+    const int e = blockIdx.x - keys, rt = e / kParts % a.row_tiles;
+    hl = e / kParts / a.row_tiles;
+    image = a.key_tiles + e % (kParts * a.row_tiles);
+    turn_query_rows<false>(a, hl, rt, e % kParts, lt, most);
+  } else {
+    hl = blockIdx.x / a.key_tiles;
+    image = blockIdx.x % a.key_tiles;
+    turn_keys<false>(a, hl, image, lt, most);
+  }
+  const int beyond = __syncthreads_or(!(most <= 65504.f));
+  if (lt == 0) a.beyond[hl * per + image] = beyond;
+}
+
+// The images of a head that exceeds fp16 again, as bf16 parts.
+__global__ void __launch_bounds__(kTurnThreads, 5) dense_wide_images_kernel(ScoreArgs a) {
+  const DenseArgs &d = a.d;
+  if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;
+  const int lt = threadIdx.x, hl = blockIdx.x / kWideBlocks, per = a.key_tiles + kParts * a.row_tiles;
+  int any = 0;
+  for (int i = lt; i < per; i += kTurnThreads) any |= __ldcg(a.beyond + hl * per + i);
+  any = __syncthreads_or(any);
+  if (lt == 0 && blockIdx.x % kWideBlocks == 0) a.wide[hl] = any;
+  if (!any) return;
+  float most = 0.f;
+  for (int i = blockIdx.x % kWideBlocks; i < per; i += kWideBlocks) {
+    if (i < a.key_tiles)
+      turn_keys<true>(a, hl, i, lt, most);
+    else
+      turn_query_rows<true>(a, hl, (i - a.key_tiles) / kParts, (i - a.key_tiles) % kParts, lt, most);
+  }
 }
 
 // A block: a range of key tiles of one (sequence, KV head) against all its query rows, 128 at a
@@ -202,7 +254,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
     mbar_fence_init();
   }
   if (warp == 8) {
-    umma::tmem_alloc(&sm.tmem, 256);
+    umma::tmem_alloc(&sm.tmem, 512);
     umma::tmem_relinquish();
   }
   if (PASS == 2)
@@ -211,6 +263,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = sm.tmem;
+  const bool wide = a.wide[hl] != 0;
+  const float unscale = wide ? 1.f : kUnscale;
   auto wait = [&](uint64_t *bar, uint32_t parity) { bounded_wait(&sm.stop, d.hdr, bar, parity); };
   // key tiles that row tile rt's queries see (at least one, so that every row tile has a product)
   auto last_tile = [&](int rt) {
@@ -221,7 +275,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
 
   if (warp < kEpilogueWarps) {
     const int set = warp >> 2, trow = (warp & 3) * 32 + lane;
-    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + set * kTile;
+    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + set * 2 * kTile;
     uint32_t n = 0;  // products so far
     for (int rt = 0; rt < a.row_tiles; ++rt) {
       const int end = last_tile(rt);
@@ -237,7 +291,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
             l += v.x != -INFINITY ? v.y * exp2_approx(v.x - m) : v.y;  // (0, or NaN: every score was)
           }
           // a row that sees nothing gives no weight; neither does a row past the queries
-          sm.lse[tid] = a.row0 + rt * kTile + tid < (d.nq << d.group_shift) && (l > 0.f || l != l) ? m + log2f(l) : INFINITY;
+          const bool gives = a.row0 + rt * kTile + tid < (d.nq << d.group_shift) && (l > 0.f || l != l);
+          sm.top[tid] = gives && l == l ? m : 0.f;
+          sm.inv[tid] = gives ? 1.f / l : 0.f;
           sm.pos[tid] = p;
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -257,11 +313,20 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           if (lane == 0) mbar_arrive(&sm.d_empty[set]);
         };
         if (PASS == 1) {
-          uint32_t s[4][32];
+          uint32_t s[4][32], more[16];
 #pragma unroll
           for (int g = 0; g < 4; ++g) umma::tmem_ld32(td + g * 32, s[g]);
-          umma::tmem_wait_ld();
-          taken();
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            tmem_ld16(td + kTile + g * 16, more);
+            umma::tmem_wait_ld();
+            if (g == 7) taken();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t &x = s[g >> 1][(g & 1) * 16 + i];
+              x = __float_as_uint((__uint_as_float(x) + __uint_as_float(more[i])) * unscale);
+            }
+          }
           const uint32_t lv[4] = {live.x, live.y, live.z, live.w};
           if (T + kTile > p_row || (live.x & live.y & live.z & live.w) != 0xffffffffu) {
 #pragma unroll
@@ -293,30 +358,35 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           // every row of the tile is a query's, and sees every key of the tile
           const bool whole = T + kTile <= p_least && a.row0 + (rt + 1) * kTile <= d.nq << d.group_shift;
           float add[4] = {};
-          uint32_t s[2][32];
-          umma::tmem_ld32(td, s[0]);
+          uint32_t s[2][16], more[2][16];
+          tmem_ld16(td, s[0]);
+          tmem_ld16(td + kTile, more[0]);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {  // 32 columns, the next 32 on their way
+          for (int g = 0; g < 8; ++g) {  // 16 columns, the next 16 on their way
             umma::tmem_wait_ld();
-            if (g < 3)
-              umma::tmem_ld32(td + (g + 1) * 32, s[(g + 1) & 1]);
-            else
+            if (g < 7) {
+              tmem_ld16(td + (g + 1) * 16, s[(g + 1) & 1]);
+              tmem_ld16(td + kTile + (g + 1) * 16, more[(g + 1) & 1]);
+            } else {
               taken();
+            }
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 z = *reinterpret_cast<const float4 *>(&sm.lse[g * 32 + i]);
-              const uint32_t *u = &s[g & 1][i];
-              float e[4] = {exp2_approx(__uint_as_float(u[0]) - z.x), exp2_approx(__uint_as_float(u[1]) - z.y),
-                            exp2_approx(__uint_as_float(u[2]) - z.z), exp2_approx(__uint_as_float(u[3]) - z.w)};
+            for (int i = 0; i < 16; i += 4) {
+              const float4 z = *reinterpret_cast<const float4 *>(&sm.top[g * 16 + i]);
+              const float4 inv = *reinterpret_cast<const float4 *>(&sm.inv[g * 16 + i]);
+              const uint32_t *u = &s[g & 1][i], *v = &more[g & 1][i];
+              auto weight = [&](int k, float top) {
+                return exp2_approx(__fmaf_rn(__uint_as_float(u[k]) + __uint_as_float(v[k]), unscale, -top));
+              };
+              float e[4] = {weight(0, z.x), weight(1, z.y), weight(2, z.z), weight(3, z.w)};
               if (!whole) {
-                const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 32 + i]);
+                const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 16 + i]);
                 if (t >= p.x) e[0] = 0.f;
                 if (t >= p.y) e[1] = 0.f;
                 if (t >= p.z) e[2] = 0.f;
                 if (t >= p.w) e[3] = 0.f;
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) add[k] += e[k];
+              add[0] += e[0] * inv.x, add[1] += e[1] * inv.y, add[2] += e[2] * inv.z, add[3] += e[3] * inv.w;
             }
           }
           if ((lw >> (trow & 31)) & 1u) sm.acc[(kt - kt0) * kTile + trow] += (add[0] + add[1]) + (add[2] + add[3]);
@@ -338,6 +408,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   } else if (warp == 8) {
     if (elect_one()) {
       const uint64_t dq = swizzled_desc(smem_u32(sm.q), 16), dk = swizzled_desc(smem_u32(sm.k[0]), 16);
+      const uint32_t idesc = wide ? chunk_idesc(kTile, true, false) : chunk_idesc(kTile, false, false);
       uint32_t n = 0;
       for (int rt = 0; rt < a.row_tiles; ++rt) {
         const int end = last_tile(rt);
@@ -351,11 +422,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           const uint64_t rows = PASS == 1 ? dq : k, cols = PASS == 1 ? k : dq;
 #pragma unroll
           for (int p = 0; p < 3; ++p) {  // small terms first: low x high, high x low, high x high
+            // the second accumulator takes the high parts' last 64 dimensions alone
             const uint64_t ra = rows + (p == 0 ? kTileBytes >> 4 : 0), cb = cols + (p == 1 ? kTileBytes >> 4 : 0);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
               const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-              umma::mma(tmem + s * kTile, ra + off, cb + off, chunk_idesc(kTile, true, false), p + ks > 0);
+              const bool second = p == 2 && ks >= 4;
+              umma::mma(tmem + (2 * s + second) * kTile, ra + off, cb + off, idesc, second ? ks > 4 : p + ks > 0);
             }
           }
           umma::commit(&sm.d_full[s]);
@@ -388,7 +461,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 8) umma::tmem_dealloc(tmem, 256);
+  if (warp == 8) umma::tmem_dealloc(tmem, 512);
 }
 
 // Weights from the scores that the rows kernel left: a thread a key.
@@ -456,23 +529,23 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
   // As many heads and rows a launch as the images' room and the sums' hold: an eighth of the room
   // for one head's rows, at least one tile of them.  Later rows add to what earlier ones wrote.  A
   // head whose images do not fit has its keys in slices, turned for pass 1 and again for pass 2.
-  constexpr int64_t kKeyBytes = kPartBytes + (int64_t)sizeof(uint4);
+  constexpr int64_t kKeyBytes = kPartBytes + (int64_t)sizeof(uint4) + 16, kRowTileBytes = kPartBytes + 16;  // with their marks
   const int64_t sums = (int64_t)kDensePartBytes / (2 * (int64_t)(kTile * sizeof(float2)));  // of a row tile and a part
   const int64_t all_tiles = ceil_div(rows, kTile);
   int64_t slice = 0, slices = 0, least = 0;  // key tiles a launch; launches a pass; fewest blocks a slice
   auto slice_for = [&](int64_t row_tiles) {
-    slice = std::min(key_tiles, (room - row_tiles * (int64_t)kPartBytes) / kKeyBytes);
+    slice = std::min(key_tiles, (room - row_tiles * kRowTileBytes) / kKeyBytes);
     if (slice < 1) return false;
     slices = ceil_div(key_tiles, slice);
     least = ceil_div(slice, kMaxRange);
     return sums / (least * slices) >= 1;
   };
   if (!slice_for(1)) return kNoRoom;
-  int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, room / 8 / kPartBytes));
+  int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, room / 8 / kRowTileBytes));
   while (tiles > 1 && (!slice_for(tiles) || tiles > sums / (least * slices))) tiles = (tiles + 1) / 2;
   slice_for(tiles);
   const int64_t key_bytes = slice * kKeyBytes;
-  const int64_t fit = slices > 1 ? 1 : std::min(room / (key_bytes + tiles * (int64_t)kPartBytes), sums / (least * tiles));
+  const int64_t fit = slices > 1 ? 1 : std::min(room / (key_bytes + tiles * kRowTileBytes), sums / (least * tiles));
   cudaError_t e = cudaFuncSetAttribute(dense_scores_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
@@ -489,6 +562,8 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
     a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
     a.query_images = a.key_images + (int64_t)a.heads * slice * kPartBytes;
     a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * tiles * kPartBytes);
+    a.beyond = reinterpret_cast<int *>(a.live + (int64_t)a.heads * slice);
+    a.wide = reinterpret_cast<int *>(reinterpret_cast<char *>(d.hdr) + kDensePrefix);
     a.sums = reinterpret_cast<float2 *>(reinterpret_cast<char *>(d.hdr) + kDensePart);
     for (int64_t rt0 = 0; rt0 < all_tiles; rt0 += tiles) {
       a.row0 = (int)(rt0 * kTile);
@@ -503,10 +578,11 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
           a.key0 = (int)(i * slice);
           a.key_tiles = (int)std::min(slice, key_tiles - i * slice);
           a.part0 = (int)(i * a.nsplit);
-          // the queries once; the keys once a pass, or once where one slice holds them all
-          const int64_t turned = i > 0 || pass > 1 ? 0 : (int64_t)a.row_tiles * (kTile / kTurnRows);
-          if (pass == 1 || slices > 1)
-            dense_score_images_kernel<<<(unsigned)(a.heads * (a.key_tiles + turned)), kTurnThreads, 0, st>>>(a);
+          if (pass == 1 || slices > 1) {  // once where one slice holds all keys
+            dense_score_images_kernel<<<(unsigned)(a.heads * (a.key_tiles + (int64_t)a.row_tiles * kParts)), kTurnThreads, 0,
+                                        st>>>(a);
+            dense_wide_images_kernel<<<(unsigned)(a.heads * kWideBlocks), kTurnThreads, 0, st>>>(a);
+          }
           const unsigned blocks = (unsigned)(a.heads * a.nsplit);
           if (pass == 1)
             dense_scores_kernel<1><<<blocks, kScoreThreads, kScoreSmem, st>>>(a);

@@ -124,8 +124,8 @@ RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const
 
 /* The softmax weight that each cache slot receives from the queries, summed over the queries
  * and over the query heads of its KV group, in fp32.
- * Up to 8 query rows a KV group, weights are as accurate as fp32 outputs above; with more, scores
- * come from two bf16 parts (2^-16).
+ * Weights are as accurate as fp32 outputs above.  (With more than 8 query rows a KV group, a head
+ * with elements beyond the parts' range is scored from two bf16 parts, 2^-16, instead.)
  *   weights : fp32 [batch][Hkv][capacity]; slots [0, L) are overwritten (accumulate = 0) or
  *             added to (accumulate = 1), slots at or past a sequence's L are left as they are.
  * Views with a window are RECSA_ERR_UNSUPPORTED, and so are more than 8 query rows a KV group

@@ -82,3 +82,61 @@ def test_one_key_beyond_the_parts_range():
     w = torch.zeros(1, 1, c.cap, device="cuda")
     R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws, view)
     assert rel(w.double().cpu(), c.want(want_weights=True, **ref)) <= 4 * 2.0 ** -21
+
+
+@pytest.mark.parametrize("sigma", [0.1, 1.0, 5.0])
+@pytest.mark.parametrize("B,H,G,L,n,page,lens", [(1, 2, 4, 4000, 3, 0, None), (2, 1, 8, 900, 40, 16, [900, 100]),
+                                                 (1, 1, 1, 3000, 200, 0, None), (3, 2, 2, 200, 9, 0, [200, 0, 5])])
+def test_weights_of_many_rows(B, H, G, L, n, page, lens, sigma):
+    c = Case(B, H, G, L, n, seed=L + n, page=page, lens=lens, scale=sigma / 1.5)
+    for own in (True, False):
+        w = torch.zeros(B, H, c.cap, device="cuda")
+        R.accumulate_weights(c.p, c.cache, c.qd, w, c.ws, R.View(causal=True, own_token=own))
+        R.check_device_errors(c.ws)
+        want = c.want(want_weights=True, causal=True, own=own)
+        assert rel(w.double().cpu(), want) <= (1 + sigma) * 2.0 ** -21
+
+
+def test_weights_of_a_head_beyond_the_parts_range():
+    """One head's keys exceed fp16, another's queries do: those come from two bf16 parts (2^-16 each
+    of scores of spread 2: 3 * 2^-16), the others keep theirs, in this call and the next."""
+    H, G, L, n = 4, 4, 700, 12
+    c = Case(1, H, G, L, n, seed=93)
+    c.k[:, 1] = (c.k[:, 1].float() * 2.0 ** 20).bfloat16()
+    c.q[:, :, G:2 * G] = (c.q[:, :, G:2 * G].float() * 2.0 ** -20).bfloat16()
+    c.k[:, 3] = (c.k[:, 3].float() * 2.0 ** -20).bfloat16()
+    c.q[:, :, 3 * G:] = (c.q[:, :, 3 * G:].float() * 2.0 ** 20).bfloat16()
+    c.cache.k_tok.copy_(c.k)
+    view = R.View(causal=True, own_token=True)
+    plain = Case(1, H, G, L, n, seed=93)
+    want = plain.want(want_weights=True, causal=True, own=True)  # powers of two cancel
+    for case, wide in ((c, (1, 3)), (plain, ()), (c, (1, 3))):
+        w = torch.zeros(1, H, c.cap, device="cuda")
+        R.accumulate_weights(c.p, case.cache, case.q.cuda(), w, c.ws, view)
+        R.check_device_errors(c.ws)
+        for h in range(H):
+            assert rel(w[0, h].double().cpu(), want[0, h]) <= (3 * 2.0 ** -16 if h in wide else 3 * 2.0 ** -21)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 3.0e38])
+@pytest.mark.parametrize("n", [2, 40])
+def test_weights_beside_a_key_that_some_queries_do_not_see(bad, n):
+    """A key beyond every range among the chunk's tokens: the queries before it weigh as without it."""
+    c = Case(1, 1, 4, 500, n, seed=94)
+    hit = 500 - n // 2
+    c.cache.k_tok[0, :, hit] = bad
+    view = R.View(causal=True)
+    few = n - n // 2  # the first queries alone: none sees the key (own tokens hidden)
+    q = c.q[:, :few].cuda().contiguous()
+    c.cache.length = 500 - n // 2
+    w = torch.zeros(1, 1, c.cap, device="cuda")
+    R.accumulate_weights(c.p, c.cache, q, w, c.ws, view)
+    c.lens, c.q = [500 - n // 2], c.q[:, :few]
+    want = c.want(causal=True, want_weights=True)
+    assert rel(w.double().cpu(), want) <= 3 * 2.0 ** -21
+    # the same queries and one that sees every token but its own: only hidden from the rest, finite
+    c.cache.length = hit + 1
+    w = torch.zeros(1, 1, c.cap, device="cuda")
+    R.accumulate_weights(c.p, c.cache, torch.cat([q, q[:, :1]], 1), w, c.ws, view)
+    R.check_device_errors(c.ws)
+    assert torch.isfinite(w).all() and (w[0, 0, hit] == 0)
