@@ -151,8 +151,8 @@ __device__ __forceinline__ void turn_queries(const DenseArgs &a, const float (*q
 // are rotated by their place in the span.  Both operands are two parts, hi * hi + lo * hi +
 // hi * lo: what is dropped is below 2^-16 of the product of the magnitudes with bf16 parts, below
 // 2^-22 with fp16 ones (EX: fp32 outputs and weights).  A rotated element beyond fp16's range makes
-// the score NaN (its second part is the opposite infinity): such a row goes to careful_row.
-// The tensor cores cut sums off: with EX the high parts are joined by rounded adds every 32 dimensions.
+// the score infinite, and that is made NaN: such a row goes to careful_row.
+// The tensor cores cut sums off: with EX they are joined by rounded adds every 32 dimensions.
 // s[nt]: keys lane/4 (first two) and lane/4 + 8, query rows nt * 8 + 2 (lane % 4) and one more.
 template <int NR, bool EX>
 __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t sk, int T, const uint32_t (&qh)[NR][16],
@@ -173,22 +173,24 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
       const float4 w = *reinterpret_cast<const float4 *>(tr + (i & 1) * 8 * kTableStride + (((2 * ks + (i >> 1)) * 64) ^ odd));
       const F2 cs = f2(w.x, w.y), sn = f2(w.z, w.w), X = f2_bf16(x[i]), Y = f2_bf16(y[i]), minus = f2(-1.f, -1.f);
       const F2 U = f2_fma(f2_mul(Y, sn), minus, f2_mul(X, cs)), V = f2_fma(X, sn, f2_mul(Y, cs));
-      split_pair<EX>(U, uh[i], ul[i]);
-      split_pair<EX>(V, vh[i], vl[i]);
+      if (EX) {
+        cut_pair(U, uh[i], ul[i]);
+        cut_pair(V, vh[i], vl[i]);
+      } else {
+        split_pair<false>(U, uh[i], ul[i]);
+        split_pair<false>(V, vh[i], vl[i]);
+      }
     }
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
-      float t[4];  // EX: these dimensions' high parts
+      float t[4];  // EX: these dimensions, small terms first
       if (EX) {
-        mma16816_half_zero(t, uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816_half_zero(t, uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
+        mma16816_half(t, vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
+        mma16816_half(t, ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
+        mma16816_half(t, vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
+        mma16816_half(t, uh, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
         mma16816_half(t, vh, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
-        if (ks == 0)
-          mma16816_half_zero(lo[nt], uh, ql[nt][0], ql[nt][1]);
-        else
-          mma16816_half(lo[nt], uh, ql[nt][2 * ks], ql[nt][2 * ks + 1]);
-        mma16816_half(lo[nt], vh, ql[nt][2 * ks + 8], ql[nt][2 * ks + 9]);
-        mma16816_half(lo[nt], ul, qh[nt][2 * ks], qh[nt][2 * ks + 1]);
-        mma16816_half(lo[nt], vl, qh[nt][2 * ks + 8], qh[nt][2 * ks + 9]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nt][i] = ks == 0 ? t[i] : s[nt][i] + t[i];
       } else {
@@ -206,11 +208,11 @@ __device__ __forceinline__ void score_step(const unsigned char *table, uint32_t 
       }
     }
   }
-  constexpr float kUnscale = EX ? 1.f / (kKeyScale * kQueryScale) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = (s[nt][i] + lo[nt][i]) * kUnscale;
+    for (int i = 0; i < 4; ++i)  // EX: an infinity becomes NaN
+      s[nt][i] = EX ? __fmaf_rn(s[nt][i], 1.f / (kKeyScale * kQueryScale), s[nt][i] * 0.f) : s[nt][i] + lo[nt][i];
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -342,7 +344,8 @@ __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg
 // fetched one step ahead with cp.async into memory of its own, so warps never wait for one another
 // until their (max, sum, output) are joined at the end; the last block of a tile joins the blocks.
 // EX: fp32's accuracy (fp32 outputs, weights).  Against two bf16 parts of everything the error of 16
-// queries over 4096 tokens fell from 6e-6 to 2.8e-7 (plain fp32 arithmetic: 7.8e-7), at the same time.
+// queries over 4096 tokens fell from 6e-6 to 3.2e-7 (plain fp32 arithmetic: 7.8e-7) at 19.3 us instead
+// of 18.4, of the weights of one step over 4 x 65536 tokens from 4.9e-6 to 2.5e-7 at 162 instead of 158.
 // Scores, probabilities and outputs are products of the tensor cores with keys (scores) and
 // dimensions (outputs) as rows and the query rows as columns, so that one to eight rows - a decode
 // step - fill an instruction.  DRAM and issue bound it together: a key of 512 bytes costs about 56
@@ -903,6 +906,7 @@ __global__ void dense_init_kernel(unsigned char *ws, double base) {
     reinterpret_cast<int32_t *>(ws + kDenseCount)[idx] = 0;
     if (idx == 0) reinterpret_cast<int32_t *>(ws + kDenseCount)[kMaxShared] = 0;
     reinterpret_cast<uint32_t *>(ws + kDenseRedo)[idx] = 0u;
+    reinterpret_cast<int32_t *>(ws + kDenseBeyond)[idx] = 0;
   }
   if (idx == 0) {
     hdr->err = 0u;

@@ -176,13 +176,25 @@ __device__ __forceinline__ F2 f2_f16(uint32_t u) {
       : "r"(u));
   return f2(lo, hi);
 }
-// Two values as the first part of an operand, and what that leaves as the second: fp16 or bf16 pairs.
+// Two values as the first part of an operand, rounded, and what that leaves as the second: pairs of
+// fp16 or bf16.
 template <bool HALF>
 __device__ __forceinline__ void split_pair(F2 x, uint32_t &hi, uint32_t &lo) {
   const float2 u = f2_get(x);
   hi = HALF ? cvt_f16x2(u.x, u.y) : cvt_bf16x2(u.x, u.y);
   const float2 d = f2_get(f2_fma(HALF ? f2_f16(hi) : f2_bf16(hi), f2(-1.f, -1.f), x));
   lo = HALF ? cvt_f16x2(d.x, d.y) : cvt_bf16x2(d.x, d.y);
+}
+// The same in fp16 with the first part cut off instead of rounded: one logical instruction, and no
+// conversion back (weights of one step over 4 x 65536 tokens 166.3 -> 162.5 us).  Second parts are up
+// to twice as large then; with the other operand's rounded, their dropped product has no bias.
+__device__ __forceinline__ void cut_pair(F2 x, uint32_t &hi, uint32_t &lo) {
+  const float2 u = f2_get(x);
+  const float2 c = make_float2(__uint_as_float(__float_as_uint(u.x) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(u.y) & 0xffffe000u));
+  const float2 d = f2_get(f2_fma(f2(c.x, c.y), f2(-1.f, -1.f), x));
+  hi = cvt_f16x2(c.x, c.y);
+  lo = cvt_f16x2(d.x, d.y);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

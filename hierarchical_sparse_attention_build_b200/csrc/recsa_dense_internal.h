@@ -19,7 +19,8 @@ constexpr size_t kDenseTableBytes = kSpan * kHalf * 2 * sizeof(float);
 constexpr size_t kDenseCount = kDenseTable + 2 * kDenseTableBytes;  // (the second table: the first times kKeyScale)
 constexpr size_t kDenseRedo = kDenseCount + kMaxShared * sizeof(int32_t) + 256;  // marks of items to compute again
 constexpr size_t kDensePrefix = kDenseRedo + kMaxShared * sizeof(uint32_t);  // key tiles before each item of a chunk
-constexpr size_t kDensePart = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // partial results
+constexpr size_t kDenseBeyond = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // heads beyond fp16: found, in use
+constexpr size_t kDensePart = kDenseBeyond + 2 * kMaxShared * sizeof(int32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
 constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
 constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a call that keeps their scores

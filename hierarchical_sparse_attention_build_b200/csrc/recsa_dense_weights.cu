@@ -14,8 +14,9 @@
 // that leaves, rounded) of scaled values and three products are summed; what is dropped is below
 // 2^-22 of the product of the magnitudes.  The tensor cores cut their sums off, toward zero, by up
 // to 2^-23 a product: a score is summed in two accumulators of 64 dimensions each, joined by a
-// rounded add (in one, 64 queries' weights over 32768 tokens were off by 1.2e-6).  A head with
-// elements that fp16 does not hold has its images made again, as two bf16 parts (2^-16).
+// rounded add.  64 queries' weights over 32768 tokens are off by 1.4e-7 (plain fp32: 1.2e-7), where
+// bf16 parts and one accumulator left 1.25e-6; that costs 173 us against 164.  A head with elements
+// that fp16 does not hold has its images made again, as two bf16 parts (2^-16).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,7 +36,7 @@ constexpr int64_t kCachedImages = (int64_t)80 << 20;  // of the 126 MB of L2
 constexpr int kTurnThreads = 128;
 constexpr int kTurnRows = 32;               // query rows a block of the images kernel turns
 constexpr int kParts = kTile / kTurnRows;   // blocks of a row tile
-constexpr int kWideBlocks = 32;             // blocks a head that make its images again
+constexpr int kWideBlocks = 32;             // blocks that make a head's images again
 constexpr float kUnscale = 1.f / (kKeyScale * kQueryScale);
 
 struct ScoreArgs {
@@ -47,7 +48,7 @@ struct ScoreArgs {
   int part0, parts;            // this launch's first of all blocks that a head's keys have in turn
   unsigned char *key_images, *query_images;  // [heads][key_tiles], [heads][row_tiles]: two parts each
   uint4 *live;                 // a key tile's tokens that were loaded
-  int *beyond;                 // [heads][key_tiles + kParts row_tiles]: an image's rows exceed fp16
+  int *beyond;                 // [heads]: some image's rows exceed fp16 (0 between calls)
   int *wide;                   // [heads]: the head's images are bf16 parts
   float2 *sums;                // [heads][row_tiles][2 parts][128]: a row's (maximum, sum) in part of the keys
   float *weights;
@@ -58,7 +59,7 @@ struct ScoreSmem {
   unsigned char q[kPartBytes];
   unsigned char k[2][kPartBytes];
   float acc[kMaxRange * kTile];  // pass 2: the block's keys
-  alignas(16) float top[kTile], inv[kTile];  // pass 2: the rows' maxima and 1 / sums
+  alignas(16) float lse[kTile];
   alignas(16) int pos[kTile];
   alignas(16) uint64_t q_full;
   uint64_t q_empty, k_full[2], k_empty[2], d_full[2], d_empty[2], drain;
@@ -66,9 +67,9 @@ struct ScoreSmem {
 };
 constexpr size_t kScoreSmem = sizeof(ScoreSmem) + 1024;
 
-// One row of 8 + 8 dimensions, times `scale`, turned, as two parts of a tile (fp16, or WIDE: bf16);
-// `most` keeps the largest magnitude.
-template <bool WIDE>
+// One row of 8 + 8 dimensions, times `scale`, turned, as two parts of a tile (fp16, of keys cut off,
+// of queries rounded; or WIDE: bf16); `most` keeps the largest magnitude.
+template <bool WIDE, bool KEY>
 __device__ __forceinline__ void put_parts(unsigned char *tile, int row, int ch, const uint4 &lo, const uint4 &hi,
                                           const Turn &t, float scale, float &most) {
   const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -83,8 +84,13 @@ __device__ __forceinline__ void put_parts(unsigned char *tile, int row, int ch, 
       const float2 x = f2_get(u), y = f2_get(v);
       most = max3(most, max3(fabsf(x.x), fabsf(x.y), fabsf(y.x)), fabsf(y.y));
     }
-    split_pair<!WIDE>(u, uh[i], ul[i]);
-    split_pair<!WIDE>(v, vh[i], vl[i]);
+    if (!WIDE && KEY) {
+      cut_pair(u, uh[i], ul[i]);
+      cut_pair(v, vh[i], vl[i]);
+    } else {
+      split_pair<!WIDE>(u, uh[i], ul[i]);
+      split_pair<!WIDE>(v, vh[i], vl[i]);
+    }
   }
   put_row(tile, row, ch, make_uint4(uh[0], uh[1], uh[2], uh[3]), make_uint4(vh[0], vh[1], vh[2], vh[3]));
   put_row(tile + kTileBytes, row, ch, make_uint4(ul[0], ul[1], ul[2], ul[3]), make_uint4(vl[0], vl[1], vl[2], vl[3]));
@@ -116,7 +122,7 @@ __device__ __forceinline__ void turn_query_rows(const ScoreArgs &a, int hl, int 
     }
     Turn t;
     t.set(f, dense_position(d, len, qi) - d.back);
-    put_parts<WIDE>(a.query_images + ((int64_t)hl * a.row_tiles + rt) * kPartBytes, in_tile, ch, lo, hi, t,
+    put_parts<WIDE, false>(a.query_images + ((int64_t)hl * a.row_tiles + rt) * kPartBytes, in_tile, ch, lo, hi, t,
                     WIDE ? d.qscale : d.qscale * kQueryScale, most);
   }
 }
@@ -157,7 +163,7 @@ __device__ __forceinline__ bool turn_keys(const ScoreArgs &a, int hl, int kt, in
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      put_parts<WIDE>(tile, r0 + 16 * (i0 + i), ch, xl[i], xh[i], t, WIDE ? 1.f : kKeyScale, most);
+      put_parts<WIDE, true>(tile, r0 + 16 * (i0 + i), ch, xl[i], xh[i], t, WIDE ? 1.f : kKeyScale, most);
       t.advance(step);
     }
   }
@@ -177,35 +183,30 @@ __device__ __forceinline__ bool turn_keys(const ScoreArgs &a, int hl, int kt, in
 __global__ void __launch_bounds__(kTurnThreads, 5) dense_score_images_kernel(ScoreArgs a) {
   const DenseArgs &d = a.d;
   if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;  // the score kernel reports it
-  const int lt = threadIdx.x, keys = a.heads * a.key_tiles, per = a.key_tiles + kParts * a.row_tiles;
+  const int lt = threadIdx.x, keys = a.heads * a.key_tiles;
   float most = 0.f;
-  int hl, image;
+  int hl;
   if ((int)blockIdx.x >= keys) {
     const int e = blockIdx.x - keys, rt = e / kParts % a.row_tiles;
     hl = e / kParts / a.row_tiles;
-    image = a.key_tiles + e % (kParts * a.row_tiles);
     turn_query_rows<false>(a, hl, rt, e % kParts, lt, most);
   } else {
     hl = blockIdx.x / a.key_tiles;
-    image = blockIdx.x % a.key_tiles;
-    turn_keys<false>(a, hl, image, lt, most);
+    turn_keys<false>(a, hl, blockIdx.x % a.key_tiles, lt, most);
   }
-  const int beyond = __syncthreads_or(!(most <= 65504.f));
-  if (lt == 0) a.beyond[hl * per + image] = beyond;
+  if (!(most <= 65504.f)) a.beyond[hl] = 1;
 }
 
 // The images of a head that exceeds fp16 again, as bf16 parts.
 __global__ void __launch_bounds__(kTurnThreads, 5) dense_wide_images_kernel(ScoreArgs a) {
   const DenseArgs &d = a.d;
   if (d.hdr->magic != kDenseMagic || d.hdr->rope_base != d.rope_base) return;
-  const int lt = threadIdx.x, hl = blockIdx.x / kWideBlocks, per = a.key_tiles + kParts * a.row_tiles;
-  int any = 0;
-  for (int i = lt; i < per; i += kTurnThreads) any |= __ldcg(a.beyond + hl * per + i);
-  any = __syncthreads_or(any);
+  const int lt = threadIdx.x, hl = blockIdx.x / kWideBlocks;
+  const int any = __ldcg(a.beyond + hl);
   if (lt == 0 && blockIdx.x % kWideBlocks == 0) a.wide[hl] = any;
   if (!any) return;
   float most = 0.f;
-  for (int i = blockIdx.x % kWideBlocks; i < per; i += kWideBlocks) {
+  for (int i = blockIdx.x % kWideBlocks; i < a.key_tiles + kParts * a.row_tiles; i += kWideBlocks) {
     if (i < a.key_tiles)
       turn_keys<true>(a, hl, i, lt, most);
     else
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
     return;
   }
   const int hl = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
+  if (PASS == 1 && split == 0 && tid == 0) a.beyond[hl] = 0;  // for the next images
   const int b = (a.bh0 + hl) / d.hkv, h = (a.bh0 + hl) % d.hkv;
   const int len = dense_length(d, b, PASS == 1 && tid == 0 && h == 0 && split == 0);
   const int tiles = min(a.key_tiles, max(0, (len + kTile - 1) / kTile - a.key0));
@@ -285,15 +287,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           const int p = row_position(d, len, a.row0 + rt * kTile + tid);
           const float2 *src = a.sums + ((int64_t)hl * a.row_tiles + rt) * (2 * a.parts) * kTile + tid;
           float m = -INFINITY, l = 0.f;
-          for (int j = 0; j < 2 * a.parts; ++j) m = fmaxf(m, __ldcg(src + j * kTile).x);
-          for (int j = 0; j < 2 * a.parts; ++j) {
-            const float2 v = __ldcg(src + j * kTile);
-            l += v.x != -INFINITY ? v.y * exp2_approx(v.x - m) : v.y;  // (0, or NaN: every score was)
+          constexpr int kAhead = 16;  // parts in flight
+          for (int j0 = 0; j0 < 2 * a.parts; j0 += kAhead) {
+            float2 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+              v[j] = j0 + j < 2 * a.parts ? __ldcg(src + (int64_t)(j0 + j) * kTile) : make_float2(-INFINITY, 0.f);
+            float top = m;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) top = fmaxf(top, v[j].x);
+            if (top > m) {
+              l *= m == -INFINITY ? 1.f : exp2_approx(m - top);  // (l is 0 or NaN without a maximum)
+              m = top;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+              l += v[j].x != -INFINITY ? v[j].y * exp2_approx(v[j].x - m) : v[j].y;  // (0, or NaN: every score was)
           }
           // a row that sees nothing gives no weight; neither does a row past the queries
           const bool gives = a.row0 + rt * kTile + tid < (d.nq << d.group_shift) && (l > 0.f || l != l);
-          sm.top[tid] = gives && l == l ? m : 0.f;
-          sm.inv[tid] = gives ? 1.f / l : 0.f;
+          sm.lse[tid] = gives ? m + log2f(l) : INFINITY;
           sm.pos[tid] = p;
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -313,80 +326,80 @@ __global__ void __launch_bounds__(kScoreThreads, 1) dense_scores_kernel(ScoreArg
           if (lane == 0) mbar_arrive(&sm.d_empty[set]);
         };
         if (PASS == 1) {
-          uint32_t s[4][32], more[16];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) umma::tmem_ld32(td + g * 32, s[g]);
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            tmem_ld16(td + kTile + g * 16, more);
-            umma::tmem_wait_ld();
-            if (g == 7) taken();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint32_t &x = s[g >> 1][(g & 1) * 16 + i];
-              x = __float_as_uint((__uint_as_float(x) + __uint_as_float(more[i])) * unscale);
-            }
-          }
           const uint32_t lv[4] = {live.x, live.y, live.z, live.w};
-          if (T + kTile > p_row || (live.x & live.y & live.z & live.w) != 0xffffffffu) {
+          const bool masked = T + kTile > p_row || (live.x & live.y & live.z & live.w) != 0xffffffffu;
+          uint32_t u[32], v[32];
+          umma::tmem_ld32(td, u);
+          umma::tmem_ld32(td + kTile, v);
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+          for (int g = 0; g < 4; ++g) {  // 32 columns, the next 32 on their way
+            float s[32];
+            umma::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = (__uint_as_float(u[i]) + __uint_as_float(v[i])) * unscale;
+            if (g < 3) {
+              umma::tmem_ld32(td + (g + 1) * 32, u);
+              umma::tmem_ld32(td + kTile + (g + 1) * 32, v);
+            } else {
+              taken();
+            }
+            if (masked) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (T + g * 32 + i >= p_row || !((lv[g] >> i) & 1u)) s[g][i] = 0xff800000u;
+                if (T + g * 32 + i >= p_row || !((lv[g] >> i) & 1u)) s[i] = -INFINITY;
+            }
+            float x[2] = {m, m};
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              x[0] = max3(x[0], s[i], s[i + 1]);
+              x[1] = max3(x[1], s[i + 2], s[i + 3]);
+            }
+            const float top = fmaxf(x[0], x[1]);
+            if (top > m) {
+              l *= m == -INFINITY ? 0.f : exp2_approx(m - top);
+              m = top;
+            }
+            const float z = m == -INFINITY ? 0.f : m;
+            float add[4] = {};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) add[i & 3] += exp2_approx(s[i] - z);
+            l += (add[0] + add[1]) + (add[2] + add[3]);
           }
-          float x[4] = {m, m, m, m};
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) x[g] = max3(x[g], __uint_as_float(s[g][i]), __uint_as_float(s[g][i + 1]));
-          const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-          if (top > m) {
-            l *= m == -INFINITY ? 0.f : exp2_approx(m - top);
-            m = top;
-          }
-          const float z = m == -INFINITY ? 0.f : m;
-          float add[4] = {};
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) add[g] += exp2_approx(__uint_as_float(s[g][i]) - z);
-          l += (add[0] + add[1]) + (add[2] + add[3]);
         } else {
           const int t = T + trow;
           const uint32_t lw = trow < 32 ? live.x : trow < 64 ? live.y : trow < 96 ? live.z : live.w;
           // every row of the tile is a query's, and sees every key of the tile
           const bool whole = T + kTile <= p_least && a.row0 + (rt + 1) * kTile <= d.nq << d.group_shift;
           float add[4] = {};
-          uint32_t s[2][16], more[2][16];
-          tmem_ld16(td, s[0]);
-          tmem_ld16(td + kTile, more[0]);
+          uint32_t u[32], v[32];
+          umma::tmem_ld32(td, u);
+          umma::tmem_ld32(td + kTile, v);
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {  // 16 columns, the next 16 on their way
+          for (int g = 0; g < 4; ++g) {  // 32 columns, the next 32 on their way
+            float s[32];
             umma::tmem_wait_ld();
-            if (g < 7) {
-              tmem_ld16(td + (g + 1) * 16, s[(g + 1) & 1]);
-              tmem_ld16(td + kTile + (g + 1) * 16, more[(g + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(u[i]) + __uint_as_float(v[i]);
+            if (g < 3) {
+              umma::tmem_ld32(td + (g + 1) * 32, u);
+              umma::tmem_ld32(td + kTile + (g + 1) * 32, v);
             } else {
               taken();
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 z = *reinterpret_cast<const float4 *>(&sm.top[g * 16 + i]);
-              const float4 inv = *reinterpret_cast<const float4 *>(&sm.inv[g * 16 + i]);
-              const uint32_t *u = &s[g & 1][i], *v = &more[g & 1][i];
-              auto weight = [&](int k, float top) {
-                return exp2_approx(__fmaf_rn(__uint_as_float(u[k]) + __uint_as_float(v[k]), unscale, -top));
-              };
-              float e[4] = {weight(0, z.x), weight(1, z.y), weight(2, z.z), weight(3, z.w)};
+            for (int i = 0; i < 32; i += 4) {
+              const float4 z = *reinterpret_cast<const float4 *>(&sm.lse[g * 32 + i]);
+              float e[4] = {exp2_approx(__fmaf_rn(s[i], unscale, -z.x)), exp2_approx(__fmaf_rn(s[i + 1], unscale, -z.y)),
+                            exp2_approx(__fmaf_rn(s[i + 2], unscale, -z.z)), exp2_approx(__fmaf_rn(s[i + 3], unscale, -z.w))};
               if (!whole) {
-                const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 16 + i]);
+                const int4 p = *reinterpret_cast<const int4 *>(&sm.pos[g * 32 + i]);
                 if (t >= p.x) e[0] = 0.f;
                 if (t >= p.y) e[1] = 0.f;
                 if (t >= p.z) e[2] = 0.f;
                 if (t >= p.w) e[3] = 0.f;
               }
-              add[0] += e[0] * inv.x, add[1] += e[1] * inv.y, add[2] += e[2] * inv.z, add[3] += e[3] * inv.w;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) add[k] += e[k];
             }
           }
           if ((lw >> (trow & 31)) & 1u) sm.acc[(kt - kt0) * kTile + trow] += (add[0] + add[1]) + (add[2] + add[3]);
@@ -529,23 +542,23 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
   // As many heads and rows a launch as the images' room and the sums' hold: an eighth of the room
   // for one head's rows, at least one tile of them.  Later rows add to what earlier ones wrote.  A
   // head whose images do not fit has its keys in slices, turned for pass 1 and again for pass 2.
-  constexpr int64_t kKeyBytes = kPartBytes + (int64_t)sizeof(uint4) + 16, kRowTileBytes = kPartBytes + 16;  // with their marks
+  constexpr int64_t kKeyBytes = kPartBytes + (int64_t)sizeof(uint4);
   const int64_t sums = (int64_t)kDensePartBytes / (2 * (int64_t)(kTile * sizeof(float2)));  // of a row tile and a part
   const int64_t all_tiles = ceil_div(rows, kTile);
   int64_t slice = 0, slices = 0, least = 0;  // key tiles a launch; launches a pass; fewest blocks a slice
   auto slice_for = [&](int64_t row_tiles) {
-    slice = std::min(key_tiles, (room - row_tiles * kRowTileBytes) / kKeyBytes);
+    slice = std::min(key_tiles, (room - row_tiles * (int64_t)kPartBytes) / kKeyBytes);
     if (slice < 1) return false;
     slices = ceil_div(key_tiles, slice);
     least = ceil_div(slice, kMaxRange);
     return sums / (least * slices) >= 1;
   };
   if (!slice_for(1)) return kNoRoom;
-  int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, room / 8 / kRowTileBytes));
+  int64_t tiles = std::min(all_tiles, std::max<int64_t>(1, room / 8 / kPartBytes));
   while (tiles > 1 && (!slice_for(tiles) || tiles > sums / (least * slices))) tiles = (tiles + 1) / 2;
   slice_for(tiles);
   const int64_t key_bytes = slice * kKeyBytes;
-  const int64_t fit = slices > 1 ? 1 : std::min(room / (key_bytes + tiles * kRowTileBytes), sums / (least * tiles));
+  const int64_t fit = slices > 1 ? 1 : std::min(room / (key_bytes + tiles * (int64_t)kPartBytes), sums / (least * tiles));
   cudaError_t e = cudaFuncSetAttribute(dense_scores_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem);
@@ -555,15 +568,15 @@ int launch_dense_weights(const DenseArgs &d, float *lse, float *weights, int acc
   // Both passes read a head's images for every row tile: heads in turn, as many as stay in the L2
   // cache from the turning to the last reading (64 queries over 8 x 32768 tokens, whose images are
   // 134 MB: 167 -> 161 us).
-  const int64_t step = std::min({heads, fit, std::max<int64_t>(1, kCachedImages / key_bytes)});
+  const int64_t step = std::min({heads, fit, std::max<int64_t>(1, kCachedImages / key_bytes), (int64_t)kMaxShared});
   for (int64_t bh0 = 0; bh0 < heads; bh0 += step) {
     a.bh0 = (int)bh0;
     a.heads = (int)std::min(step, heads - bh0);
     a.key_images = reinterpret_cast<unsigned char *>(d.hdr) + kDenseImages;
     a.query_images = a.key_images + (int64_t)a.heads * slice * kPartBytes;
     a.live = reinterpret_cast<uint4 *>(a.query_images + (int64_t)a.heads * tiles * kPartBytes);
-    a.beyond = reinterpret_cast<int *>(a.live + (int64_t)a.heads * slice);
-    a.wide = reinterpret_cast<int *>(reinterpret_cast<char *>(d.hdr) + kDensePrefix);
+    a.beyond = reinterpret_cast<int *>(reinterpret_cast<char *>(d.hdr) + kDenseBeyond);
+    a.wide = a.beyond + kMaxShared;
     a.sums = reinterpret_cast<float2 *>(reinterpret_cast<char *>(d.hdr) + kDensePart);
     for (int64_t rt0 = 0; rt0 < all_tiles; rt0 += tiles) {
       a.row0 = (int)(rt0 * kTile);
