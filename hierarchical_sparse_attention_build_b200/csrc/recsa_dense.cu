@@ -264,9 +264,8 @@ struct Dealt {
 
 // One row over the steps [begin, stop) of its tile by one warp, in fp32: dimensions 4 lane .. 4 lane
 // + 3 of the weighted sum of values (without PV: the scores, written), the weights' sum and the
-// maximum they are relative to.  Every
-// value is weighed by itself: one that the row does not see is not touched, and an infinity does
-// not meet the zero that a weight's second part may be.
+// maximum they are relative to.  Every value is weighed by itself: one that the row does not see is
+// not touched, and an infinity does not meet the zero that a weight's second part may be.
 template <int R, bool PV, bool EX>
 __device__ void careful_row(const DenseArgs &a, RowsSmem<R> &sm, const Range &rg, int row, int b, int h, int p_max,
                             int base_sink, int bh, float (&acc)[4], float &m, float &sum) {

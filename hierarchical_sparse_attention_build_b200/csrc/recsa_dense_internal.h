@@ -22,8 +22,8 @@ constexpr size_t kDensePrefix = kDenseRedo + kMaxShared * sizeof(uint32_t);  // 
 constexpr size_t kDenseBeyond = kDensePrefix + (kMaxShared + 64) * sizeof(int32_t);  // heads beyond fp16: found, in use
 constexpr size_t kDensePart = kDenseBeyond + 2 * kMaxShared * sizeof(int32_t);  // partial results
 constexpr size_t kDensePartBytes = (size_t)40 << 20;
-constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // float a query row
-constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // query rows of a call that keeps their scores
+constexpr size_t kDenseLse = kDensePart + kDensePartBytes;                 // two floats a query row
+constexpr int64_t kMaxDenseLse = (int64_t)1 << 20;                         // floats: rows of a call that keeps their scores
 constexpr size_t kDenseImages = kDenseLse + kMaxDenseLse * sizeof(float);   // rotated rows of a chunk's keys and queries
 constexpr size_t kMaxDenseImages = (size_t)320 << 20;   // for many heads together
 constexpr size_t kMaxHeadImages = (size_t)1280 << 20;   // for one long head
@@ -66,7 +66,7 @@ inline int redo_slot(int bh, int tiles, int tile) { return (int)(((int64_t)bh * 
 
 int dense_sm_count();  // of the current device
 int launch_dense_init(void *ws, double base, void *stream);
-// The rows kernel: outputs, or with `lse` the rows' log2-sum-exp (at most 8 rows a KV group).
+// The rows kernel: outputs, or with `lse` the rows' (maximum, 1 / sum) (at most 8 rows a KV group).
 int launch_dense_rows(DenseArgs a, int64_t max_keys, float *lse, void *stream);
 // The chunk kernel (bf16 output), then the rows kernel for the items it marked; kNoRoom, with
 // nothing launched, where a head's rotated keys do not fit image_bytes of the workspace.

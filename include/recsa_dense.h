@@ -114,7 +114,8 @@ RECSA_API recsa_status recsa_dense_prefill_chunk(const recsa_params *params, rec
 /* recsa_decode_step's dense counterpart: per sequence appends one token at its device length,
  * advances the length and attends that token's query over the tokens it then holds (its own
  * included).  Every launch parameter comes from the capacity, so the call can be captured into
- * a CUDA graph.  Needs tree->seq_len; tree->length is neither read nor written.  A sequence
+ * a CUDA graph.  Needs tree->seq_len; tree->length is neither read nor written (the other calls
+ * take it as the lengths' bound: the caller sets it before them).  A sequence
  * with no room keeps its tokens and length and is flagged (RECSA_ERR_DEVICE_CHECK).
  * view->causal is not used; own_token = 2 puts the query at its own token's position. */
 RECSA_API recsa_status recsa_dense_decode_step(const recsa_params *params, const recsa_tree *tree,
